@@ -123,9 +123,9 @@ def _parameters(A, D, dt_bias, H) -> int:
 class _Batch:
     """Packed inputs of the scan; [B, T, ...] input becomes B sequences of T tokens."""
 
-    __slots__ = ("batch", "x", "dt", "B", "C", "cu", "more", "rows", "H", "P", "G", "N", "seqs", "args")
+    __slots__ = ("batch", "x", "dt", "B", "C", "cu", "rows", "H", "P", "G", "N", "seqs", "args")
 
-    def __init__(self, x, dt, A, B, C, cu_seqlens, D, dt_bias, dt_softplus, *more):
+    def __init__(self, x, dt, A, B, C, cu_seqlens, D, dt_bias, dt_softplus):
         self.batch = None
         if x.dim() == 4:
             if cu_seqlens is not None:
@@ -134,10 +134,9 @@ class _Batch:
             self.batch = (b, t)
             cu_seqlens = torch.arange(b + 1, dtype=torch.int32, device=x.device) * t
             x, dt, B, C = (self.flat(v) for v in (x, dt, B, C))
-            more = tuple(None if v is None else self.flat(v) for v in more)
         if cu_seqlens is None:
             cu_seqlens = torch.tensor([0, x.shape[0]], dtype=torch.int32, device=x.device)
-        self.x, self.dt, self.B, self.C, self.cu, self.more = x, dt, B, C, cu_seqlens, more
+        self.x, self.dt, self.B, self.C, self.cu = x, dt, B, C, cu_seqlens
         (xs, x_sizes), (bs, b_sizes), (cs, c_sizes) = _rows3s(x, "x"), _rows3s(B, "B"), _rows3s(C, "C")
         rows, H, P = self.rows, self.H, self.P = x_sizes
         _, G, N = b_sizes
@@ -149,7 +148,20 @@ class _Batch:
                      A.data_ptr(), _at(D), _at(dt_bias), _parameters(A, D, dt_bias, H), B.data_ptr(), bs, C.data_ptr(), cs, G, N)
 
     def flat(self, t):
-        return t.reshape(self.batch[0] * self.batch[1], *t.shape[2:])
+        """An input packed; a copy where batch and time do not follow each other in memory."""
+        return t if self.batch is None else t.reshape(self.batch[0] * self.batch[1], *t.shape[2:])
+
+    def place(self, t, sizes, name):
+        """What is written, packed: the caller's memory, or new (t is None)."""
+        if t is None:
+            return self.x.new_empty(sizes)
+        if self.batch is None:
+            return t
+        try:
+            return t.view(self.batch[0] * self.batch[1], *t.shape[2:])
+        except RuntimeError:
+            raise ValueError(f"{name} {tuple(t.shape)} with strides {t.stride()} is written in place: batch and time must follow "
+                             "each other in memory (a view as [B T, ...])") from None
 
     def unflat(self, t):
         return t if self.batch is None else t.view(*self.batch, *t.shape[1:])
@@ -188,11 +200,8 @@ def selective_scan_fn(x, dt, A, B, C, ssm_state=None, cu_seqlens=None, cache_ind
         if ssm_state.dtype != _F32 or ssm_state.shape[1:] != (H, P, N) or not (slots == 0 or ssm_state[0].is_contiguous()):
             raise ValueError("ssm_state must be FP32 [slots, H, P, N] with contiguous slots")
         st_slot = ssm_state.stride(0) if slots > 1 else H * P * N
-    if out is None:
-        o, os = b.x.new_empty((b.rows, H, P)), H * P
-    else:
-        o = out if b.batch is None else b.flat(out)
-        os = _rows3(o, "out", (b.rows, H, P), "out must match x")
+    o = b.place(out, (b.rows, H, P), "out")
+    os = H * P if out is None else _rows3(o, "out", (b.rows, H, P), "out must match x")
     b.states(initial_state, "initial_state")
     b.states(final_state, "final_state")
     workspace = b.workspace(workspace, 0)
@@ -212,12 +221,9 @@ def selective_scan_bwd(x, dt, A, B, C, dy, cu_seqlens=None, *, D=None, dt_bias=N
     """Selective scan backward (include/ccc.h, ccc_scan_bwd).  ``dx``, ``dB``
     and ``dC`` may be given, also as column slices of one buffer (the dy of
     ccc_bwd); rows past cu_seqlens[-1] of what is made here are not written."""
-    b = _Batch(x, dt, A, B, C, cu_seqlens, D, dt_bias, dt_softplus, dy, dx, dB, dC)
-    dy2, dx2, dB2, dC2 = b.more
+    b = _Batch(x, dt, A, B, C, cu_seqlens, D, dt_bias, dt_softplus)
     wide, narrow, new = (b.rows, b.H, b.P), (b.rows, b.G, b.N), b.x.new_empty
-    dx2 = new(wide) if dx2 is None else dx2
-    dB2 = new(narrow) if dB2 is None else dB2
-    dC2 = new(narrow) if dC2 is None else dC2
+    dy2, dx2, dB2, dC2 = b.flat(dy), b.place(dx, wide, "dx"), b.place(dB, narrow, "dB"), b.place(dC, narrow, "dC")
     match = "dy and dx must match x, dB and dC must match B"
     strides = [_rows3(dy2, "dy", wide, match), _rows3(dx2, "dx", wide, match), _rows3(dB2, "dB", narrow, match), _rows3(dC2, "dC", narrow, match)]
     ddt = new((b.rows, b.H), dtype=b.dt.dtype)
