@@ -120,6 +120,13 @@ def _parameters(A, D, dt_bias, H) -> int:
     return _code(A, "A, D and dt_bias")
 
 
+def _metadata(t, name, need, types=(torch.int32,)) -> None:
+    """The library gets a bare pointer: a tensor of another type, layout or of fewer elements would be read as something else."""
+    if t is not None and (t.dtype not in types or t.numel() < need or not t.is_contiguous()):
+        what = " or ".join(str(v).removeprefix("torch.") for v in types)
+        raise ValueError(f"{name} must be contiguous {what} of {need} elements, got {t.dtype} {tuple(t.shape)}")
+
+
 class _Batch:
     """Packed inputs of the scan; [B, T, ...] input becomes B sequences of T tokens."""
 
@@ -144,6 +151,7 @@ class _Batch:
         if b_sizes[0] != rows or c_sizes != b_sizes:
             raise ValueError("x [rows, H, P], B and C [rows, G, N] do not match")
         self.seqs = cu_seqlens.numel() - 1
+        _metadata(cu_seqlens, "cu_seqlens", 1)
         self.args = (x.data_ptr(), rows, H, P, xs, dt.data_ptr(), _code(dt, "dt"), _steps(dt, rows, H), 1 if dt_softplus else 0,
                      A.data_ptr(), _at(D), _at(dt_bias), _parameters(A, D, dt_bias, H), B.data_ptr(), bs, C.data_ptr(), cs, G, N)
 
@@ -200,6 +208,8 @@ def selective_scan_fn(x, dt, A, B, C, ssm_state=None, cu_seqlens=None, cache_ind
         if ssm_state.dtype != _F32 or ssm_state.shape[1:] != (H, P, N) or not (slots == 0 or ssm_state[0].is_contiguous()):
             raise ValueError("ssm_state must be FP32 [slots, H, P, N] with contiguous slots")
         st_slot = ssm_state.stride(0) if slots > 1 else H * P * N
+    _metadata(cache_indices, "cache_indices", b.seqs)
+    _metadata(has_initial_state, "has_initial_state", b.seqs, (torch.bool, torch.uint8))
     o = b.place(out, (b.rows, H, P), "out")
     os = H * P if out is None else _rows3(o, "out", (b.rows, H, P), "out must match x")
     b.states(initial_state, "initial_state")
@@ -222,6 +232,7 @@ def selective_scan_bwd(x, dt, A, B, C, dy, cu_seqlens=None, *, D=None, dt_bias=N
     and ``dC`` may be given, also as column slices of one buffer (the dy of
     ccc_bwd); rows past cu_seqlens[-1] of what is made here are not written."""
     b = _Batch(x, dt, A, B, C, cu_seqlens, D, dt_bias, dt_softplus)
+    _metadata(cache_indices, "cache_indices", b.seqs)
     wide, narrow, new = (b.rows, b.H, b.P), (b.rows, b.G, b.N), b.x.new_empty
     dy2, dx2, dB2, dC2 = b.flat(dy), b.place(dx, wide, "dx"), b.place(dB, narrow, "dB"), b.place(dC, narrow, "dC")
     match = "dy and dx must match x, dB and dC must match B"
@@ -299,6 +310,10 @@ def ssm_update(xBC, weight, conv_state, dt, A, ssm_state, cache_indices, *, n_gr
     elif cu_seqlens is None:
         cu_seqlens = torch.arange(xBC.shape[0] + 1, dtype=torch.int32, device=xBC.device)
     xs, (rows, channels) = _rows2s(xBC, "xBC")
+    seqs = cu_seqlens.numel() - 1
+    _metadata(cu_seqlens, "cu_seqlens", 1)
+    _metadata(cache_indices, "cache_indices", seqs)
+    _metadata(num_accepted, "num_accepted", seqs)
     if ssm_state.dtype != _F32 or ssm_state.dim() not in (4, 5):
         raise ValueError("ssm_state must be FP32 [slots, H, P, N] or [slots, positions, H, P, N]")
     G = int(n_groups)
@@ -329,7 +344,7 @@ def ssm_update(xBC, weight, conv_state, dt, A, ssm_state, cache_indices, *, n_gr
         xBC.data_ptr(), rows, H, P, G, N, xs, weight.data_ptr(), _code(weight), weight.shape[1], _at(bias), -1 if bias is None else _code(bias),
         _act_code(activation), _at(conv_state), slots, L, st[0], st[1], st[2], dt.data_ptr(), _code(dt, "dt"), _steps(dt, rows, H),
         1 if dt_softplus else 0, A.data_ptr(), _at(D), _at(dt_bias), _parameters(A, D, dt_bias, H), ssm_state.data_ptr(), held, st_slot, st_pos,
-        cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, _at(cache_indices), _at(num_accepted), y.data_ptr(), os, _stream(stream)))
+        cu_seqlens.data_ptr(), seqs, _at(cache_indices), _at(num_accepted), y.data_ptr(), os, _stream(stream)))
     if rc != 0:
         raise CCCError(rc, "ccc_ssm_update")
     if out is not None:

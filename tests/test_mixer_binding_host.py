@@ -36,3 +36,57 @@ def test_written_in_place_or_refused(name):
     for good in (b16(2, 5, heads, per), b16(2, 5, heads * per + 16)[..., :heads * per].unflatten(2, (heads, per))):
         with pytest.raises(ValueError, match="CUDA tensors"):
             call(good)
+
+
+def packed(**kw):
+    """The same as three packed sequences of ten rows."""
+    a = dict(x=b16(10, 4, 64), dt=torch.zeros(10, 4), A=torch.zeros(4), B=b16(10, 2, 128), C=b16(10, 2, 128), cu_seqlens=ints(4))
+    a.update(kw)
+    return a
+
+
+def ints(n, dtype=torch.int32):
+    return torch.zeros(n, dtype=dtype)
+
+
+def step(**kw):
+    a = dict(xBC=b16(3, 768), weight=torch.zeros(768, 4), conv_state=b16(8, 768, 5), dt=torch.zeros(3, 4), A=torch.zeros(4), ssm_state=torch.zeros(8, 2, 4, 64, 128),
+             cache_indices=ints(3), n_groups=2, cu_seqlens=ints(4), num_accepted=ints(3), bias=b16(768))
+    a.update(kw)
+    return a
+
+
+NOT_INT32 = [ints(3, torch.int64), ints(6)[::2], ints(2)]  # another type, a stride, too short
+
+
+@pytest.mark.parametrize("bad", [ints(4, torch.int64), ints(8)[::2], ints(0)])
+def test_cu_seqlens_type_and_layout(bad):
+    for call in (lambda: ccc.selective_scan_fn(**packed(cu_seqlens=bad)), lambda: ccc.selective_scan_bwd(**packed(cu_seqlens=bad), dy=b16(10, 4, 64)),
+                 lambda: ccc.ssm_update(**step(cu_seqlens=bad))):
+        with pytest.raises(ValueError, match="cu_seqlens must"):
+            call()
+
+
+@pytest.mark.parametrize("bad", NOT_INT32)
+def test_slots_and_counts_type_and_length(bad):
+    for call in (lambda: ccc.selective_scan_fn(**packed(), cache_indices=bad), lambda: ccc.selective_scan_bwd(**packed(), dy=b16(10, 4, 64), cache_indices=bad),
+                 lambda: ccc.ssm_update(**step(cache_indices=bad))):
+        with pytest.raises(ValueError, match="cache_indices must"):
+            call()
+    with pytest.raises(ValueError, match="num_accepted must"):
+        ccc.ssm_update(**step(num_accepted=bad))
+
+
+@pytest.mark.parametrize("bad", [ints(3), torch.zeros(3), ints(2, torch.bool), ints(6, torch.bool)[::2]])
+def test_flags_type_and_length(bad):
+    with pytest.raises(ValueError, match="has_initial_state must"):
+        ccc.selective_scan_fn(**packed(), has_initial_state=bad)
+
+
+def test_metadata_that_fits_is_taken():
+    """Flags as bool or bytes, and arrays longer than the batch, as a padded batch has them."""
+    for flags in (ints(3, torch.bool), ints(5, torch.uint8)):
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            ccc.selective_scan_fn(**packed(), cache_indices=ints(5), has_initial_state=flags)
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        ccc.ssm_update(**step(cache_indices=ints(5), num_accepted=ints(5)))
