@@ -331,6 +331,8 @@ def ssm_update(xBC, weight, conv_state, dt, A, ssm_state, cache_indices, *, n_gr
     st_slot = s[0] if slots > 1 else held * st_pos
     if channels != H * P + 2 * G * N or weight.dim() != 2 or weight.shape[0] != channels:
         raise ValueError("xBC [rows, H P + 2 G N] and weight [C, W] do not match ssm_state and n_groups")
+    if not weight.is_contiguous() or (bias is not None and (bias.numel() != channels or not bias.is_contiguous())):
+        raise ValueError("weight [C, W] and bias [C] must be contiguous")
     c_slots, L, st = _pool_args(conv_state, channels)
     if c_slots != slots:
         raise ValueError("conv_state and ssm_state must have the same slots")

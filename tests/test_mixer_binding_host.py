@@ -90,3 +90,11 @@ def test_metadata_that_fits_is_taken():
             ccc.selective_scan_fn(**packed(), cache_indices=ints(5), has_initial_state=flags)
     with pytest.raises(ValueError, match="CUDA tensors"):
         ccc.ssm_update(**step(cache_indices=ints(5), num_accepted=ints(5)))
+
+
+@pytest.mark.parametrize("bad", [dict(weight=torch.zeros(4, 768).t()), dict(weight=torch.zeros(768, 8)[:, ::2]), dict(bias=b16(700)), dict(bias=b16(1)),
+                                 dict(bias=b16(1536)[::2])])
+def test_convolution_parameters_of_a_step(bad):
+    """The taps are read as [C, W] and the bias as [C], whatever their strides and sizes say."""
+    with pytest.raises(ValueError, match="must be contiguous"):
+        ccc.ssm_update(**step(**bad))
