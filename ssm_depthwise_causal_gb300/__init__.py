@@ -39,6 +39,7 @@ gated RMS norm behind the scan (``gated_rms_norm_fn`` / ``gated_rms_norm_bwd``
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
@@ -135,6 +136,20 @@ def _stream(stream) -> int:
             return _raw_current_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _under_stream(call):
+    """A function that makes tensors and takes ``stream=`` runs under that stream: what it makes (workspace, offsets, flat
+    copies, results) is allocated, written and freed in its order, not in the current stream's."""
+    @functools.wraps(call)
+    def under(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream))
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return under
 
 
 def _rows_view(t: torch.Tensor, name: str):

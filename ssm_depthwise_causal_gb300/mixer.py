@@ -5,7 +5,9 @@ the one-launch decode step (``ccc_ssm_update``) and the gated RMS norm
 
 As in the package's other entry points, every function marshals torch tensors
 into pointers, sizes and strides and calls the library on the current stream;
-outputs and workspaces are created when they are not given.
+outputs and workspaces are created when they are not given.  ``stream=s`` (a
+stream or its handle) is the call under ``with torch.cuda.stream(s)``: what it
+makes belongs to that stream, and what it is given has to be ready there.
 """
 from __future__ import annotations
 
@@ -15,7 +17,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import CCCError, _act_code, _lib, _on_current_device, _pool_args, _stream
+from . import CCCError, _act_code, _lib, _on_current_device, _pool_args, _stream, _under_stream
 
 __all__ = ["ScanGrads", "SelectiveScanFn", "GatedRMSNormFn", "ccc_scan_workspace_size", "ccc_gated_norm_workspace_size",
            "selective_scan_fn", "selective_scan_bwd", "selective_scan", "ssm_update", "gated_rms_norm_fn",
@@ -190,9 +192,10 @@ def _bytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
+@_under_stream
 def selective_scan_fn(x, dt, A, B, C, ssm_state=None, cu_seqlens=None, cache_indices=None, has_initial_state=None, *,
                       D=None, dt_bias=None, dt_softplus=False, initial_state=None, final_state=None, out=None,
-                      workspace=None, stream=None) -> torch.Tensor:
+                      workspace=None) -> torch.Tensor:
     """Selective scan forward (include/ccc.h, ccc_scan_fwd): y, shaped as x.
 
     ``x`` [rows, H, P], ``dt`` [rows, H], ``B`` and ``C`` [rows, G, N] are
@@ -219,15 +222,16 @@ def selective_scan_fn(x, dt, A, B, C, ssm_state=None, cu_seqlens=None, cache_ind
                        o, workspace)
     rc = _lib.lib().ccc_scan_fwd_v(_PACK[33](
         *b.args, _at(ssm_state), slots, st_slot, _at(initial_state), _at(final_state), b.cu.data_ptr(), b.seqs, _at(cache_indices),
-        _at(has_initial_state), o.data_ptr(), os, _at(workspace), _bytes(workspace), _stream(stream)))
+        _at(has_initial_state), o.data_ptr(), os, _at(workspace), _bytes(workspace), _stream(None)))
     if rc != 0:
         raise CCCError(rc, "ccc_scan_fwd")
     return b.unflat(o) if out is None else out
 
 
+@_under_stream
 def selective_scan_bwd(x, dt, A, B, C, dy, cu_seqlens=None, *, D=None, dt_bias=None, dt_softplus=False, initial_state=None,
                        cache_indices=None, d_final_state=None, want_d_initial=False, dx=None, dB=None, dC=None,
-                       workspace=None, stream=None) -> ScanGrads:
+                       workspace=None) -> ScanGrads:
     """Selective scan backward (include/ccc.h, ccc_scan_bwd).  ``dx``, ``dB``
     and ``dC`` may be given, also as column slices of one buffer (the dy of
     ccc_bwd); rows past cu_seqlens[-1] of what is made here are not written."""
@@ -249,7 +253,7 @@ def selective_scan_bwd(x, dt, A, B, C, dy, cu_seqlens=None, *, D=None, dt_bias=N
     rc = _lib.lib().ccc_scan_bwd_v(_PACK[41](
         *b.args, _at(initial_state), b.cu.data_ptr(), b.seqs, _at(cache_indices), dy2.data_ptr(), strides[0], _at(d_final_state),
         dx2.data_ptr(), strides[1], ddt.data_ptr(), b.H, dB2.data_ptr(), strides[2], dC2.data_ptr(), strides[3], dA.data_ptr(), _at(dD),
-        _at(dbias), _at(d_init), _at(workspace), _bytes(workspace), _stream(stream)))
+        _at(dbias), _at(d_init), _at(workspace), _bytes(workspace), _stream(None)))
     if rc != 0:
         raise CCCError(rc, "ccc_scan_bwd")
     return ScanGrads(b.unflat(dx2) if dx is None else dx, b.unflat(ddt), dA, b.unflat(dB2) if dB is None else dB,
@@ -293,8 +297,9 @@ def selective_scan(x, dt, A, B, C, cu_seqlens=None, *, D=None, dt_bias=None, dt_
     return SelectiveScanFn.apply(x, dt, A, B, C, D, dt_bias, initial_state, cu_seqlens, cache_indices, dt_softplus)
 
 
+@_under_stream
 def ssm_update(xBC, weight, conv_state, dt, A, ssm_state, cache_indices, *, n_groups, cu_seqlens=None, num_accepted=None,
-               bias=None, activation="silu", D=None, dt_bias=None, dt_softplus=False, out=None, stream=None) -> torch.Tensor:
+               bias=None, activation="silu", D=None, dt_bias=None, dt_softplus=False, out=None) -> torch.Tensor:
     """One decode step of the mixer (include/ccc.h, ccc_ssm_update): y
     [rows, H, P] (or [B, k, H, P]) of the new tokens ``xBC`` [rows, C] with
     ``cu_seqlens`` ([B, C]: one token a request; [B, k, C]: k of them), with
@@ -346,7 +351,7 @@ def ssm_update(xBC, weight, conv_state, dt, A, ssm_state, cache_indices, *, n_gr
         xBC.data_ptr(), rows, H, P, G, N, xs, weight.data_ptr(), _code(weight), weight.shape[1], _at(bias), -1 if bias is None else _code(bias),
         _act_code(activation), _at(conv_state), slots, L, st[0], st[1], st[2], dt.data_ptr(), _code(dt, "dt"), _steps(dt, rows, H),
         1 if dt_softplus else 0, A.data_ptr(), _at(D), _at(dt_bias), _parameters(A, D, dt_bias, H), ssm_state.data_ptr(), held, st_slot, st_pos,
-        cu_seqlens.data_ptr(), seqs, _at(cache_indices), _at(num_accepted), y.data_ptr(), os, _stream(stream)))
+        cu_seqlens.data_ptr(), seqs, _at(cache_indices), _at(num_accepted), y.data_ptr(), os, _stream(None)))
     if rc != 0:
         raise CCCError(rc, "ccc_ssm_update")
     if out is not None:
@@ -375,7 +380,8 @@ def _norm_args(y, z, weight, group_size, eps, norm_before_gate):
             1 if norm_before_gate else 0), sizes
 
 
-def gated_rms_norm_fn(y, z, weight, *, eps=1e-5, group_size=None, norm_before_gate=False, out=None, stream=None) -> torch.Tensor:
+@_under_stream
+def gated_rms_norm_fn(y, z, weight, *, eps=1e-5, group_size=None, norm_before_gate=False, out=None) -> torch.Tensor:
     """Gated RMS norm (include/ccc.h, ccc_gated_norm_fwd) of y by the gate z,
     both BF16 [..., width]; ``group_size`` defaults to the whole width."""
     y2, z2 = _flat2(y), _flat2(z)
@@ -386,14 +392,15 @@ def gated_rms_norm_fn(y, z, weight, *, eps=1e-5, group_size=None, norm_before_ga
         o = out if out.dim() == 2 else out.view(sizes)
         os = _rows2(o, "out", sizes, "out must match y")
     _on_current_device(y2, z2, weight, o)
-    rc = _lib.lib().ccc_gated_norm_fwd_v(_PACK[14](*args, o.data_ptr(), os, _stream(stream)))
+    rc = _lib.lib().ccc_gated_norm_fwd_v(_PACK[14](*args, o.data_ptr(), os, _stream(None)))
     if rc != 0:
         raise CCCError(rc, "ccc_gated_norm_fwd")
     return out if out is not None else o if y2 is y else o.view(y.shape)
 
 
+@_under_stream
 def gated_rms_norm_bwd(y, z, weight, dout, *, eps=1e-5, group_size=None, norm_before_gate=False, dy=None, dz=None,
-                       workspace=None, stream=None):
+                       workspace=None):
     """(dy, dz, dweight) of gated_rms_norm_fn; dweight is FP32 [width]."""
     y2, z2, g2 = _flat2(y), _flat2(z), _flat2(dout)
     args, sizes = _norm_args(y2, z2, weight, group_size, eps, norm_before_gate)
@@ -407,7 +414,7 @@ def gated_rms_norm_bwd(y, z, weight, dout, *, eps=1e-5, group_size=None, norm_be
         workspace = y2.new_empty(need, dtype=torch.uint8)
     _on_current_device(y2, z2, weight, g2, a, b, workspace)
     rc = _lib.lib().ccc_gated_norm_bwd_v(_PACK[21](*args, g2.data_ptr(), gs, a.data_ptr(), strides[0], b.data_ptr(), strides[1], dw.data_ptr(),
-                                                   _at(workspace), _bytes(workspace), _stream(stream)))
+                                                   _at(workspace), _bytes(workspace), _stream(None)))
     if rc != 0:
         raise CCCError(rc, "ccc_gated_norm_bwd")
     return (a.view(y.shape) if dy is None else dy), (b.view(y.shape) if dz is None else dz), dw
