@@ -27,9 +27,10 @@ The width W is the second dimension of ``weight`` ([C, W], W in 2..4) and
 ``core.ssm.causal_conv1d``, causal_conv1d_cp).  On top: the allocating
 conveniences ``causal_conv1d_fn`` / ``causal_conv1d_bwd`` /
 ``causal_conv1d_update``, which create outputs and the workspace when they
-are not given and accept ``[B, T, D]`` (non-packed) input as well as packed
-``[rows, C]``; ``recompute_fwd`` (bitwise re-run of a forward from its saved
-history) and the autograd wrapper ``causal_conv1d`` / ``CausalConv1dFn``.
+are not given (under ``stream=`` where that is given) and accept
+``[B, T, D]`` (non-packed) input as well as packed ``[rows, C]``;
+``recompute_fwd`` (bitwise re-run of a forward from its saved history) and the
+autograd wrapper ``causal_conv1d`` / ``CausalConv1dFn``.
 
 Around the convolution (``mixer.py``): the selective scan that reads its
 output (``selective_scan_fn`` / ``selective_scan_bwd`` / ``selective_scan``),
@@ -282,7 +283,7 @@ def ccc_check(rows, cu_seqlens, cache_indices=None, n_slots=0, num_accepted=None
     N = cu_seqlens.numel() - 1
     words = int(_lib.lib().ccc_check_status_words(int(n_slots))) if cache_indices is not None else 1
     if status is None:
-        status = torch.empty(words, dtype=torch.int32, device=cu_seqlens.device)
+        status = _under_stream(torch.empty)(words, dtype=torch.int32, device=cu_seqlens.device, stream=stream)
     if status.dtype != torch.int32 or not status.is_contiguous():
         raise ValueError("status must be a contiguous int32 tensor")
     _on_current_device(cu_seqlens, cache_indices, num_accepted, status)
@@ -328,9 +329,10 @@ def _packed(x, cu_seqlens):
     return x2, cu_seqlens, (lambda t: t.view(x.shape) if x.dim() == 3 else t)
 
 
+@_under_stream
 def causal_conv1d_fn(x, weight, conv_state=None, cu_seqlens=None, cache_indices=None,
                      has_initial_state=None, *, bias=None, activation="silu", out=None,
-                     workspace=None, saved_hist=None, stream=None) -> torch.Tensor:
+                     workspace=None, saved_hist=None) -> torch.Tensor:
     """Allocating forward: ``out`` and the workspace are created when omitted
     (rows past cu_seqlens[-1] of an ``out`` made here hold whatever the
     allocator left).  ``x`` is
@@ -341,13 +343,14 @@ def causal_conv1d_fn(x, weight, conv_state=None, cu_seqlens=None, cache_indices=
     o2 = torch.empty_like(x2) if out is None else out.reshape(rows, C)
     workspace = _workspace(rows, N, C, False, x.device, workspace)
     ccc_fwd(x2, weight, bias, conv_state, cu, cache_indices, has_initial_state, o2,
-            saved_hist, workspace, stream, activation)
+            saved_hist, workspace, None, activation)
     return unpack(o2) if out is None else out
 
 
+@_under_stream
 def causal_conv1d_bwd(x, weight, dy, cu_seqlens=None, *, bias=None, activation="silu",
                       saved_hist=None, cache_indices=None, has_initial_state=None,
-                      d_final_state=None, dx=None, want_d_init=False, workspace=None, stream=None):
+                      d_final_state=None, dx=None, want_d_init=False, workspace=None):
     """Allocating backward: returns ``(dx, dweight, dbias, d_init_state)``
     (dweight FP32 [C, W]; dbias None without a bias, d_init_state
     [N, W-1, C] only when requested)."""
@@ -363,13 +366,13 @@ def causal_conv1d_bwd(x, weight, dy, cu_seqlens=None, *, bias=None, activation="
     d_init = torch.empty((N, W - 1, C), dtype=torch.float32, device=dev) if want_d_init else None
     workspace = _workspace(rows, N, C, True, dev, workspace)
     ccc_bwd(x2, weight, bias, saved_hist, cu, cache_indices, has_initial_state, g2,
-            d_final_state, d2, dweight, dbias, d_init, workspace, stream, activation)
+            d_final_state, d2, dweight, dbias, d_init, workspace, None, activation)
     return (unpack(d2) if dx is None else dx), dweight, dbias, d_init
 
 
+@_under_stream
 def causal_conv1d_update(x, weight, conv_state, cache_indices, *, cu_seqlens=None,
-                         num_accepted=None, bias=None, activation="silu", out=None,
-                         stream=None) -> torch.Tensor:
+                         num_accepted=None, bias=None, activation="silu", out=None) -> torch.Tensor:
     """Allocating decode step: ``x`` is ``[B, k, D]`` (k new tokens for each
     of B sequences; [B, D] means k = 1) or packed ``[rows, C]`` with
     ``cu_seqlens``; ``conv_state`` is updated in place (ccc_update)."""
@@ -378,7 +381,7 @@ def causal_conv1d_update(x, weight, conv_state, cache_indices, *, cu_seqlens=Non
         x = x.unsqueeze(1)   # [B, D]: one token per sequence
     x2, cu, unpack = _packed(x, cu_seqlens)
     o2 = torch.empty_like(x2)
-    ccc_update(x2, weight, bias, conv_state, cu, cache_indices, num_accepted, o2, stream, activation)
+    ccc_update(x2, weight, bias, conv_state, cu, cache_indices, num_accepted, o2, None, activation)
     y = unpack(o2)
     if squeeze:
         y = y.reshape(y.shape[0], y.shape[-1])
@@ -388,8 +391,9 @@ def causal_conv1d_update(x, weight, conv_state, cache_indices, *, cu_seqlens=Non
     return y
 
 
+@_under_stream
 def recompute_fwd(x, weight, saved_hist, cu_seqlens, cache_indices=None, *, bias=None,
-                  activation="silu", out=None, workspace=None, stream=None) -> torch.Tensor:
+                  activation="silu", out=None, workspace=None) -> torch.Tensor:
     """Re-run the forward from the history a previous ccc_fwd saved.
 
     ``saved_hist`` [N, W-1, C] is read as a pool of N slots (slot n =
@@ -405,7 +409,7 @@ def recompute_fwd(x, weight, saved_hist, cu_seqlens, cache_indices=None, *, bias
         slots = torch.where(cache_indices == -1, cache_indices, slots)
     every = torch.ones(N, dtype=torch.bool, device=x.device)
     return causal_conv1d_fn(x, weight, pool, cu_seqlens, slots, every, bias=bias, activation=activation,
-                            out=out, workspace=workspace, stream=stream)
+                            out=out, workspace=workspace)
 
 
 class CausalConv1dFn(torch.autograd.Function):
