@@ -422,7 +422,11 @@ int ccc_check(int64_t rows, const int32_t *cu_seqlens, int32_t N,
  * -1 request), and of A, D, dt_bias and the initial state in FP32, overwritten
  * and summed in a fixed order without atomics: repeated calls match bit for
  * bit.  d_final_state [N][H][P][N_state] (or NULL) is the gradient of the
- * final state; d_initial_state is 0 for empty sequences and -1 requests.
+ * final state.  d_initial_state is the gradient through a sequence's tokens: 0
+ * for empty sequences and -1 requests.  An empty sequence also hands its initial
+ * state on as its final one; CCC_OPT_CARRY_EMPTY adds that path, so that its
+ * d_initial_state is its d_final_state (0 without one), as a chain of fragments
+ * needs it.  -1 requests hand nothing on: 0 either way.
  * initial_state is what the forward started from (zeros where
  * has_initial_state was false).  dD may be NULL if D is, d_dt_bias if dt_bias
  * is.
@@ -454,6 +458,21 @@ int ccc_scan_bwd(const void *x, int64_t rows, int32_t H, int32_t P, int64_t x_ro
                  void *dB, int64_t db_row_stride, void *dC, int64_t dc_row_stride,
                  float *dA, float *dD, float *d_dt_bias, float *d_initial_state,
                  void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/* ccc_scan_bwd with options.  Unknown bits (CCC_OPT_OVERLAP_PROLOGUE among them) return CCC_ERR_SHAPE. */
+enum { CCC_OPT_CARRY_EMPTY = 1 << 1 };
+
+int ccc_scan_bwd_ex(const void *x, int64_t rows, int32_t H, int32_t P, int64_t x_row_stride,
+                    const void *dt, int32_t dt_dtype, int64_t dt_row_stride, int32_t dt_softplus,
+                    const void *A, const void *D, const void *dt_bias, int32_t p_dtype,
+                    const void *B, int64_t b_row_stride, const void *C, int64_t c_row_stride, int32_t G, int32_t N_state,
+                    const float *initial_state,
+                    const int32_t *cu_seqlens, int32_t N, const int32_t *cache_indices,
+                    const void *dy, int64_t dy_row_stride, const float *d_final_state,
+                    void *dx, int64_t dx_row_stride, void *ddt, int64_t ddt_row_stride,
+                    void *dB, int64_t db_row_stride, void *dC, int64_t dc_row_stride,
+                    float *dA, float *dD, float *d_dt_bias, float *d_initial_state,
+                    void *workspace, size_t workspace_bytes, uint32_t options, void *cuda_stream);
 
 /*
  * Decode step of the whole mixer in one launch: ccc_update on the channels
@@ -515,11 +534,12 @@ int ccc_gated_norm_bwd(const void *y, int64_t rows, int32_t width, int64_t y_row
 /*
  * The calls above with their arguments, in their order, as an array of 64-bit
  * integers (pointers as addresses, eps as the bits of its float): 33 of
- * ccc_scan_fwd, 41 of ccc_scan_bwd, 38 of ccc_ssm_update, 14 and 21 of the
- * norms.  For bindings whose cost grows with the number of arguments.
+ * ccc_scan_fwd, 41 of ccc_scan_bwd, 42 of ccc_scan_bwd_ex, 38 of ccc_ssm_update,
+ * 14 and 21 of the norms.  For bindings whose cost grows with the number of arguments.
  */
 int ccc_scan_fwd_v(const int64_t *args);
 int ccc_scan_bwd_v(const int64_t *args);
+int ccc_scan_bwd_ex_v(const int64_t *args);
 int ccc_ssm_update_v(const int64_t *args);
 int ccc_gated_norm_fwd_v(const int64_t *args);
 int ccc_gated_norm_bwd_v(const int64_t *args);

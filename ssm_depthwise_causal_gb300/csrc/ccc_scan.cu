@@ -95,8 +95,10 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const ScanArgs a, bool
     const int64_t head = static_cast<int64_t>(h) * P * N;
     const bool dead = scan_padded(a, n);
     if (s.end == s.begin || dead) {
-        if (reverse && a.d_initial)
-            for (int i = threadIdx.x; i < P * N; i += kThreads) a.d_initial[n * hpn + head + i] = 0.0f;
+        if (reverse && a.d_initial) {
+            const float *from = scan_edge_gradient(a, n, dead);
+            for (int i = threadIdx.x; i < P * N; i += kThreads) a.d_initial[n * hpn + head + i] = from ? from[head + i] : 0.0f;
+        }
         if (!reverse && !a.pool && a.final_state) {
             // an empty sequence hands its initial state on, a padded request none
             const float *from = dead ? nullptr : scan_initial(a, n);

@@ -31,6 +31,7 @@ struct ScanArgs {
     int64_t out_rs;
     // backward
     const float *d_final;
+    int carry_empty;       // CCC_OPT_CARRY_EMPTY: an empty sequence's d_initial is its d_final, not zeros
     uint16_t *dx, *dB, *dC;
     int64_t dx_rs, db_rs, dc_rs, ddt_rs;
     void *ddt;

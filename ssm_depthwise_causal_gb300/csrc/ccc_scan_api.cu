@@ -165,7 +165,7 @@ int ccc_scan_fwd(const void *x, int64_t rows, int32_t H, int32_t P, int64_t x_ro
     return CCC_OK;
 }
 
-int ccc_scan_bwd(const void *x, int64_t rows, int32_t H, int32_t P, int64_t x_row_stride,
+int ccc_scan_bwd_ex(const void *x, int64_t rows, int32_t H, int32_t P, int64_t x_row_stride,
                  const void *dt, int32_t dt_dtype, int64_t dt_row_stride, int32_t dt_softplus,
                  const void *A, const void *D, const void *dt_bias, int32_t p_dtype,
                  const void *B, int64_t b_row_stride, const void *C, int64_t c_row_stride, int32_t G, int32_t N_state,
@@ -175,7 +175,8 @@ int ccc_scan_bwd(const void *x, int64_t rows, int32_t H, int32_t P, int64_t x_ro
                  void *dx, int64_t dx_row_stride, void *ddt, int64_t ddt_row_stride,
                  void *dB, int64_t db_row_stride, void *dC, int64_t dc_row_stride,
                  float *dA, float *dD, float *d_dt_bias, float *d_initial_state,
-                 void *workspace, size_t workspace_bytes, void *cuda_stream) {
+                 void *workspace, size_t workspace_bytes, uint32_t options, void *cuda_stream) {
+    if (options & ~static_cast<uint32_t>(CCC_OPT_CARRY_EMPTY)) return CCC_ERR_SHAPE;
     ScanArgs a = {};
     a.x = static_cast<const uint16_t *>(x);
     a.dt = dt;
@@ -198,6 +199,7 @@ int ccc_scan_bwd(const void *x, int64_t rows, int32_t H, int32_t P, int64_t x_ro
     a.cache = cache_indices;
     a.initial = initial_state;
     a.d_final = d_final_state;
+    a.carry_empty = (options & CCC_OPT_CARRY_EMPTY) != 0;
     a.dx = static_cast<uint16_t *>(dx);
     a.dB = static_cast<uint16_t *>(dB);
     a.dC = static_cast<uint16_t *>(dC);
@@ -238,13 +240,16 @@ int ccc_scan_bwd(const void *x, int64_t rows, int32_t H, int32_t P, int64_t x_ro
     }
     set_last_launches(0);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-    if (rows == 0 || N == 0) {  // no token: the gradients are zero
+    if (rows == 0 || N == 0) {  // no token: the gradients are zero, but for what an empty sequence hands on
         const size_t bytes = static_cast<size_t>(H) * 4;
         if (cudaMemsetAsync(dA, 0, bytes, st) != cudaSuccess || (dD && cudaMemsetAsync(dD, 0, bytes, st) != cudaSuccess) ||
-            (d_dt_bias && cudaMemsetAsync(d_dt_bias, 0, bytes, st) != cudaSuccess) ||
-            (d_initial_state && N > 0 &&
-             cudaMemsetAsync(d_initial_state, 0, static_cast<size_t>(N) * hpn * 4, st) != cudaSuccess))
+            (d_dt_bias && cudaMemsetAsync(d_dt_bias, 0, bytes, st) != cudaSuccess))
             return CCC_ERR_CUDA;
+        if (!d_initial_state || N == 0) return CCC_OK;
+        if (!a.carry_empty)
+            return cudaMemsetAsync(d_initial_state, 0, static_cast<size_t>(N) * hpn * 4, st) == cudaSuccess ? CCC_OK : CCC_ERR_CUDA;
+        if (launch_edge_states(a, d_initial_state, true, st) != cudaSuccess) return CCC_ERR_CUDA;
+        set_last_launches(1);
         return CCC_OK;
     }
     unsigned char *ws = static_cast<unsigned char *>(workspace);
@@ -268,8 +273,27 @@ int ccc_scan_bwd(const void *x, int64_t rows, int32_t H, int32_t P, int64_t x_ro
     return CCC_OK;
 }
 
+int ccc_scan_bwd(const void *x, int64_t rows, int32_t H, int32_t P, int64_t x_row_stride,
+                 const void *dt, int32_t dt_dtype, int64_t dt_row_stride, int32_t dt_softplus,
+                 const void *A, const void *D, const void *dt_bias, int32_t p_dtype,
+                 const void *B, int64_t b_row_stride, const void *C, int64_t c_row_stride, int32_t G, int32_t N_state,
+                 const float *initial_state,
+                 const int32_t *cu_seqlens, int32_t N, const int32_t *cache_indices,
+                 const void *dy, int64_t dy_row_stride, const float *d_final_state,
+                 void *dx, int64_t dx_row_stride, void *ddt, int64_t ddt_row_stride,
+                 void *dB, int64_t db_row_stride, void *dC, int64_t dc_row_stride,
+                 float *dA, float *dD, float *d_dt_bias, float *d_initial_state,
+                 void *workspace, size_t workspace_bytes, void *cuda_stream) {
+    return ccc_scan_bwd_ex(x, rows, H, P, x_row_stride, dt, dt_dtype, dt_row_stride, dt_softplus, A, D, dt_bias, p_dtype, B, b_row_stride, C,
+                           c_row_stride, G, N_state, initial_state, cu_seqlens, N, cache_indices, dy, dy_row_stride, d_final_state, dx,
+                           dx_row_stride, ddt, ddt_row_stride, dB, db_row_stride, dC, dc_row_stride, dA, dD, d_dt_bias, d_initial_state, workspace,
+                           workspace_bytes, 0, cuda_stream);
+}
+
 int ccc_scan_fwd_v(const int64_t *args) { return call_packed(ccc_scan_fwd, args); }
 
 int ccc_scan_bwd_v(const int64_t *args) { return call_packed(ccc_scan_bwd, args); }
+
+int ccc_scan_bwd_ex_v(const int64_t *args) { return call_packed(ccc_scan_bwd_ex, args); }
 
 }  // extern "C"

@@ -56,6 +56,12 @@ __device__ __forceinline__ float *scan_final(const ScanArgs &a, int n) {
     return a.final_state && !scan_padded(a, n) ? a.final_state + static_cast<int64_t>(n) * a.H * a.P * a.N : nullptr;
 }
 
+// The gradient of the initial state of a sequence without rows (null: zeros).  An empty sequence's final state is its
+// initial one; a padded request's is zeros whatever it started from.
+__device__ __forceinline__ const float *scan_edge_gradient(const ScanArgs &a, int n, bool dead) {
+    return a.carry_empty && a.d_final && !dead ? a.d_final + static_cast<int64_t>(n) * a.H * a.P * a.N : nullptr;
+}
+
 // The step of dt_raw + dt_bias.  log1p(exp(v)) is v to the last bit of 32 for v > 20.
 __device__ __forceinline__ float step_of(float v, int softplus) {
     return !softplus || v > 20.0f ? v : log1pf(expf(v));

@@ -43,8 +43,8 @@ cudaError_t launch_scan_tc_tails(ScanTcArgs a, const ScanTcPlan &plan, bool reve
 cudaError_t launch_scan_tc_states(const ScanArgs &a, const ScanTcPlan &plan, unsigned char *workspace, bool reverse, uint16_t *store,
                                   int *launches, cudaStream_t st);
 
-// What a walk does not meet: the final states (zero: gradients of initial states) of sequences without rows and padded requests.
-cudaError_t launch_edge_states(const ScanArgs &a, float *to, bool zero, cudaStream_t st);
+// What a walk does not meet: the final states (gradient: gradients of initial states) of sequences without rows and padded requests.
+cudaError_t launch_edge_states(const ScanArgs &a, float *to, bool gradient, cudaStream_t st);
 
 // The backward's workspace behind the plan's, and its launches.
 struct ScanTcBwdPlan {

@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) states_kernel(const __grid_consta
     if (tid == 0 && *failed) *a.status = 1;
 }
 
-__global__ void edge_states_kernel(const ScanArgs a, float *to, bool zero) {
+__global__ void edge_states_kernel(const ScanArgs a, float *to, bool gradient) {
     grid_dependents_launch();
     grid_dependency_wait();
     const int n = blockIdx.x;
@@ -409,7 +409,7 @@ __global__ void edge_states_kernel(const ScanArgs a, float *to, bool zero) {
     const bool dead = scan_padded(a, n);
     if (s.end > s.begin && !dead) return;
     const int64_t hpn = static_cast<int64_t>(a.H) * a.P * a.N;
-    const float *from = zero || dead ? nullptr : scan_initial(a, n);
+    const float *from = gradient ? scan_edge_gradient(a, n, dead) : dead ? nullptr : scan_initial(a, n);
     for (int64_t i = threadIdx.x; i < hpn; i += blockDim.x) to[n * hpn + i] = from ? from[i] : 0.0f;
 }
 
@@ -422,8 +422,8 @@ cudaError_t launch_states(const ScanTcArgs &a, const ScanTcPlan &plan, bool reve
 
 }  // namespace
 
-cudaError_t launch_edge_states(const ScanArgs &a, float *to, bool zero, cudaStream_t st) {
-    edge_states_kernel<<<a.n_seqs, 256, 0, st>>>(a, to, zero);
+cudaError_t launch_edge_states(const ScanArgs &a, float *to, bool gradient, cudaStream_t st) {
+    edge_states_kernel<<<a.n_seqs, 256, 0, st>>>(a, to, gradient);
     return cudaGetLastError();
 }
 

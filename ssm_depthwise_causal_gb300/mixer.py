@@ -50,7 +50,7 @@ def ccc_gated_norm_workspace_size(rows, width, group_size) -> int:
 
 # The arguments of a call as one array of 64-bit integers (the _v entry points
 # of include/ccc.h): packing them costs a fraction of converting each one.
-_PACK = {n: struct.Struct(f"{n}q").pack for n in (14, 21, 33, 38, 41)}
+_PACK = {n: struct.Struct(f"{n}q").pack for n in (14, 21, 33, 38, 42)}
 
 _F32, _BF16 = torch.float32, torch.bfloat16
 _CODE = {torch.float32: 0, torch.bfloat16: 1}
@@ -230,11 +230,15 @@ def selective_scan_fn(x, dt, A, B, C, ssm_state=None, cu_seqlens=None, cache_ind
 
 @_under_stream
 def selective_scan_bwd(x, dt, A, B, C, dy, cu_seqlens=None, *, D=None, dt_bias=None, dt_softplus=False, initial_state=None,
-                       cache_indices=None, d_final_state=None, want_d_initial=False, dx=None, dB=None, dC=None,
-                       workspace=None) -> ScanGrads:
+                       cache_indices=None, d_final_state=None, want_d_initial=False, carry_empty=False, dx=None, dB=None,
+                       dC=None, workspace=None) -> ScanGrads:
     """Selective scan backward (include/ccc.h, ccc_scan_bwd).  ``dx``, ``dB``
     and ``dC`` may be given, also as column slices of one buffer (the dy of
-    ccc_bwd); rows past cu_seqlens[-1] of what is made here are not written."""
+    ccc_bwd); rows past cu_seqlens[-1] of what is made here are not written.
+    ``d_initial`` is the gradient through a sequence's tokens; ``carry_empty``
+    adds that of an empty sequence, whose final state is its initial one (its
+    d_final_state as it is): pass it where fragments are chained, as the
+    autograd wrapper does."""
     b = _Batch(x, dt, A, B, C, cu_seqlens, D, dt_bias, dt_softplus)
     _metadata(cache_indices, "cache_indices", b.seqs)
     wide, narrow, new = (b.rows, b.H, b.P), (b.rows, b.G, b.N), b.x.new_empty
@@ -250,10 +254,10 @@ def selective_scan_bwd(x, dt, A, B, C, dy, cu_seqlens=None, *, D=None, dt_bias=N
     b.states(d_final_state, "d_final_state")
     workspace = b.workspace(workspace, 1)
     _on_current_device(b.x, b.dt, A, b.B, b.C, b.cu, D, dt_bias, initial_state, cache_indices, dy2, d_final_state, dx2, dB2, dC2, workspace)
-    rc = _lib.lib().ccc_scan_bwd_v(_PACK[41](
+    rc = _lib.lib().ccc_scan_bwd_ex_v(_PACK[42](
         *b.args, _at(initial_state), b.cu.data_ptr(), b.seqs, _at(cache_indices), dy2.data_ptr(), strides[0], _at(d_final_state),
         dx2.data_ptr(), strides[1], ddt.data_ptr(), b.H, dB2.data_ptr(), strides[2], dC2.data_ptr(), strides[3], dA.data_ptr(), _at(dD),
-        _at(dbias), _at(d_init), _at(workspace), _bytes(workspace), _stream(None)))
+        _at(dbias), _at(d_init), _at(workspace), _bytes(workspace), _lib.OPT_CARRY_EMPTY if carry_empty else 0, _stream(None)))
     if rc != 0:
         raise CCCError(rc, "ccc_scan_bwd")
     return ScanGrads(b.unflat(dx2) if dx is None else dx, b.unflat(ddt), dA, b.unflat(dB2) if dB is None else dB,
@@ -281,7 +285,7 @@ class SelectiveScanFn(torch.autograd.Function):
         made = [torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (x, B, C)]
         g = selective_scan_bwd(x, dt, A, B, C, dy.contiguous(), cu, D=D, dt_bias=dt_bias, dt_softplus=ctx.dt_softplus,
                                initial_state=initial, cache_indices=cache, d_final_state=d_final.contiguous(),
-                               want_d_initial=initial is not None, dx=made[0], dB=made[1], dC=made[2])
+                               want_d_initial=initial is not None, carry_empty=True, dx=made[0], dB=made[1], dC=made[2])
         ddt = g.ddt
         if cu is not None:  # as above, for the rows past the last sequence
             ddt = torch.where(torch.arange(dt.shape[0], device=dt.device)[:, None] < cu[-1], ddt, torch.zeros_like(ddt))

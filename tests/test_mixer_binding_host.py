@@ -98,3 +98,18 @@ def test_convolution_parameters_of_a_step(bad):
     """The taps are read as [C, W] and the bias as [C], whatever their strides and sizes say."""
     with pytest.raises(ValueError, match="must be contiguous"):
         ccc.ssm_update(**step(**bad))
+
+
+def test_backward_options_are_checked():
+    """ccc_scan_bwd_ex knows one bit; what it does not know is refused before anything else, and the array form agrees."""
+    import struct
+
+    from ssm_depthwise_causal_gb300 import _build, _lib
+    from tests.test_host import E_NULL, E_SHAPE
+    from tests.test_mixer_host import BWD
+    _build.build()
+    for bits, want in ((1, E_SHAPE), (4, E_SHAPE), (3, E_SHAPE), (_lib.OPT_CARRY_EMPTY, E_NULL), (0, E_NULL)):
+        args = [*dict(BWD, dA=0).values()]
+        args.insert(-1, bits)
+        assert _lib.lib().ccc_scan_bwd_ex(*args) == want
+        assert _lib.lib().ccc_scan_bwd_ex_v(struct.pack("42q", *args)) == want
