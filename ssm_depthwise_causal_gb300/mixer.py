@@ -16,6 +16,7 @@ import struct
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import CCCError, _act_code, _lib, _on_current_device, _pool_args, _stream, _under_stream
 
@@ -266,7 +267,8 @@ def selective_scan_bwd(x, dt, A, B, C, dy, cu_seqlens=None, *, D=None, dt_bias=N
 
 class SelectiveScanFn(torch.autograd.Function):
     """Autograd wrapper: (y, final_state) of selective_scan_fn; the backward
-    recomputes the states, so nothing of the forward is kept but its inputs."""
+    recomputes the states, so nothing of the forward is kept but its inputs.
+    A second derivative is refused."""
 
     @staticmethod
     def forward(ctx, x, dt, A, B, C, D, dt_bias, initial_state, cu_seqlens, cache_indices, dt_softplus):
@@ -280,6 +282,7 @@ class SelectiveScanFn(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, d_final):
         x, dt, A, B, C, D, dt_bias, initial, cu, cache = ctx.saved_tensors
         made = [torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (x, B, C)]
@@ -425,7 +428,8 @@ def gated_rms_norm_bwd(y, z, weight, dout, *, eps=1e-5, group_size=None, norm_be
 
 
 class GatedRMSNormFn(torch.autograd.Function):
-    """Autograd wrapper: recomputes from y and z, keeps nothing else."""
+    """Autograd wrapper: recomputes from y and z, keeps nothing else.  A second
+    derivative is refused."""
 
     @staticmethod
     def forward(ctx, y, z, weight, eps, group_size, norm_before_gate):
@@ -434,6 +438,7 @@ class GatedRMSNormFn(torch.autograd.Function):
         return gated_rms_norm_fn(y, z, weight, **ctx.kind)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         y, z, weight = ctx.saved_tensors
         dy, dz, dw = gated_rms_norm_bwd(y, z, weight, dout.contiguous(), **ctx.kind)
