@@ -310,8 +310,9 @@ def ssm_update(xBC, weight, conv_state, dt, A, ssm_state, cache_indices, *, n_gr
     """One decode step of the mixer (include/ccc.h, ccc_ssm_update): y
     [rows, H, P] (or [B, k, H, P]) of the new tokens ``xBC`` [rows, C] with
     ``cu_seqlens`` ([B, C]: one token a request; [B, k, C]: k of them), with
-    both pools updated in place.  ``ssm_state`` is [slots, H, P, N], or
-    [slots, positions, H, P, N] to keep every draft token's state."""
+    both pools updated in place.  ``ssm_state`` is [slots, H, P, N] for one
+    token a request, or [slots, positions, H, P, N] to keep the states after a
+    request's first ``positions`` tokens (of which num_accepted then names one)."""
     lead = None
     if xBC.dim() == 3:
         lead = xBC.shape[:2]
@@ -331,6 +332,9 @@ def ssm_update(xBC, weight, conv_state, dt, A, ssm_state, cache_indices, *, n_gr
     G = int(n_groups)
     s = ssm_state.stride()
     if ssm_state.dim() == 4:
+        if rows > seqs:
+            raise ValueError(f"{rows} tokens of {seqs} requests: ssm_state [slots, H, P, N] has room for the state after one token; pass "
+                             "[slots, positions, H, P, N]")
         slots, H, P, N = ssm_state.shape
         held, hpn = 1, H * P * N
         st_pos = hpn

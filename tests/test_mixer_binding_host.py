@@ -113,3 +113,16 @@ def test_backward_options_are_checked():
         args.insert(-1, bits)
         assert _lib.lib().ccc_scan_bwd_ex(*args) == want
         assert _lib.lib().ccc_scan_bwd_ex_v(struct.pack("42q", *args)) == want
+
+
+def test_several_tokens_need_positions():
+    """A pool without positions would keep the state after a request's first token alone."""
+    flat = torch.zeros(8, 4, 64, 128)
+    for call in (lambda: ccc.ssm_update(**step(ssm_state=flat, xBC=b16(6, 768), dt=torch.zeros(6, 4))),
+                 lambda: ccc.ssm_update(**step(ssm_state=flat, xBC=b16(3, 2, 768), dt=torch.zeros(3, 2, 4), cu_seqlens=None))):
+        with pytest.raises(ValueError, match="room for the state after one token"):
+            call()
+    for good in (step(ssm_state=flat), step(ssm_state=flat, xBC=b16(2, 768), dt=torch.zeros(2, 4)), step(ssm_state=flat, cu_seqlens=None),
+                 step(ssm_state=flat[:, None], xBC=b16(6, 768), dt=torch.zeros(6, 4)), step(xBC=b16(3, 2, 768), dt=torch.zeros(3, 2, 4), cu_seqlens=None)):
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            ccc.ssm_update(**good)
