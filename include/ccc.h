@@ -482,16 +482,19 @@ int ccc_scan_bwd_ex(const void *x, int64_t rows, int32_t H, int32_t P, int64_t x
  * in ccc_update's output.
  *
  *  xBC          [dev] BF16 [rows][x_row_stride], raw channels x, B, C.
- *  weight .. st_l, cu_seqlens, cache_indices, num_accepted: as in ccc_update.
+ *  weight .. st_l, cu_seqlens, cache_indices, num_accepted: as in ccc_update,
+ *               but for num_accepted's upper limit (below).
  *  dt .. p_dtype: as in ccc_scan_fwd.
  *  ssm_state    [dev] FP32 pool, required: position p of slot q at
  *               q*ssm_st_slot + p*ssm_st_pos, then [H][P][N_state]
  *               contiguous; ssm_len >= 1 positions.  With a = num_accepted[n]
- *               (1 if NULL, clamped to [1, ssm_len]) the step starts from
+ *               (1 if NULL, clamped to [1, min(ssm_len, state_len - W + 2)],
+ *               the positions that both pools have) the step starts from
  *               position a-1, the state after the a-th token of the previous
  *               step, and leaves the state after its own j-th token in
  *               position j, j < ssm_len.  A prefill's final state belongs in
- *               position 0.
+ *               position 0.  A request whose accepted count may reach k needs
+ *               ssm_len >= k and state_len >= k + W - 2.
  *  out          [dev] BF16 [rows][out_row_stride]: y, H*P channels.
  */
 int ccc_ssm_update(const void *xBC, int64_t rows, int32_t H, int32_t P, int32_t G, int32_t N_state, int64_t x_row_stride,

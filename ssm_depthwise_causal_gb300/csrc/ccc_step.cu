@@ -86,9 +86,8 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
             s.out[(seq.begin + i / xw) * s.out_rs + h0 * s.P + i % xw] = 0;
         return;
     }
-    // accepted counts: clamped for each pool to the positions that it has
-    const int acc = max(a.accepted ? a.accepted[n] : 1, 1);
-    const int acc_c = min(acc, a.state_len - a.width + 2), acc_s = min(acc, a.held);
+    // the accepted count, clamped to the positions that both pools have: history and state are those behind the same token
+    const int acc = min(max(a.accepted ? a.accepted[n] : 1, 1), min(a.state_len - a.width + 2, a.held));
     float *pool = s.pool + slot * s.st_slot + static_cast<int64_t>(h0) * s.P * s.N;
     const int pieces = (xw + kPiece - 1) / kPiece;
     // With more tokens than are staged at a time, the convolution is computed again for every piece, by every CTA of the
@@ -98,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
         const uint32_t bar = smem_addr(&s_full[i % kStages]);
         const uint32_t bytes = static_cast<uint32_t>(min(kPiece, xw - i * kPiece)) * s.N * 4;
         bar_expect(bar, bytes);
-        bulk_load(smem_addr(state + i % kStages * kPiece * s.N), pool + (acc_s - 1) * a.st_pos + static_cast<int64_t>(i) * kPiece * s.N, bytes, bar);
+        bulk_load(smem_addr(state + i % kStages * kPiece * s.N), pool + (acc - 1) * a.st_pos + static_cast<int64_t>(i) * kPiece * s.N, bytes, bar);
     };
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) bar_init(smem_addr(&s_full[i]), 1);
@@ -132,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
                     for (int k = 0; k < 4; ++k) tap[k] = k < a.width ? par(a.w, a.w_bf16, c * a.width + k) : 0.0f;
 #pragma unroll
                     for (int k = 0; k < 3; ++k) {  // (past the first tokens the window is all tokens)
-                        old[k] = k < a.width - 1 ? (t0 == 0 ? past[(acc_c - 1 + k) * a.st_l] : x[(k + 1 - a.width) * a.xs]) : uint16_t{0};
+                        old[k] = k < a.width - 1 ? (t0 == 0 ? past[(acc - 1 + k) * a.st_l] : x[(k + 1 - a.width) * a.xs]) : uint16_t{0};
                         win[k] = bf_to_f(old[k]);
                     }
                     for (int j = 0; j < nt; ++j) {
