@@ -102,6 +102,11 @@ struct Walk {
             if (in_pair) {
                 n += REV ? -1 : 1;
                 s = scan_seq(a, n);
+                if (s.end == s.begin) {  // over a run of empty ones at once: others wait for this with a limit
+                    const int to = warp_find_seq(a, REV ? s.begin - 1 : s.begin);
+                    n = REV ? min(n, to) : max(n, to);
+                    s = scan_seq(a, n);
+                }
                 place();
                 continue;
             }

@@ -94,3 +94,43 @@ def test_a_chain_of_fragments_with_an_empty_one():
     torch.cat(ys).backward(g.dy)
     off = (first.grad.double().cpu() - want["d_initial"]).abs() - 2 ** -14 * mag["d_initial"] - 1e-30
     assert bool((off <= 0).all())
+
+
+def with_empty_runs(c, runs):
+    """The same batch with `runs[i]` empty sequences before sequence i, and the last count behind all."""
+    lengths = [0] * runs[0]
+    for n, more in zip(c.lengths, runs[1:]):
+        lengths += [n] + [0] * more
+    cu = torch.zeros(len(lengths) + 1, dtype=torch.int64)
+    cu[1:] = torch.tensor(lengths).cumsum(0)
+    return cu.to(torch.int32).cuda()
+
+
+@pytest.mark.parametrize("runs", [[3, 0, 40, 1, 2], [300, 1000, 33, 2000, 700]])
+def test_runs_of_empty_sequences(runs):
+    """They change nothing, forward or backward, in either direction of the walks."""
+    c = ref.make([20, 1800, 128, 700], 2, 64, 1, 128, seed=35)
+    g, want, mag = c.to("cuda"), ref.scan(c, grad=True), ref.scan(c, grad=True, mag=True)
+    cu = with_empty_runs(c, runs)
+    par = dict(D=g.D, dt_bias=g.dt_bias, dt_softplus=True)
+    y = ccc.selective_scan_fn(g.x, g.dt, g.A, g.B, g.C, None, cu, **par)
+    d = ccc.selective_scan_bwd(g.x, g.dt, g.A, g.B, g.C, g.dy, cu, **par)
+    for got, name, eps in ((y, "y", 2 ** -7), (d.dx, "dx", 2 ** -6), (d.dB, "dB", 2 ** -6), (d.dC, "dC", 2 ** -6)):  # as in test_mixer_gpu
+        off = (got.double().cpu() - want[name]).abs() - eps * mag[name] - 1e-30
+        assert bool((off <= 0).all()), name
+    assert float((d.dA.double().cpu() - want["dA"]).norm()) <= 2 ** -13 * float(mag["dA"].norm())
+
+
+def test_a_million_empty_sequences():
+    """A walk steps over a run of them at once: one by one would take as long as its other warps wait at most."""
+    c = ref.make([40, 1500, 30], 2, 64, 1, 128, seed=36)
+    g, want, mag = c.to("cuda"), ref.scan(c)["y"], ref.scan(c, mag=True)["y"]
+    cu = with_empty_runs(c, [1_000_000, 0, 1_000_000, 5])
+    y = ccc.selective_scan_fn(g.x, g.dt, g.A, g.B, g.C, None, cu, D=g.D, dt_bias=g.dt_bias, dt_softplus=True)
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    ccc.selective_scan_fn(g.x, g.dt, g.A, g.B, g.C, None, cu, D=g.D, dt_bias=g.dt_bias, dt_softplus=True)
+    end.record()
+    torch.cuda.synchronize()
+    assert bool(((y.double().cpu() - want).abs() <= 2 ** -7 * mag + 1e-30).all())
+    assert begin.elapsed_time(end) < 50.0  # ms; a step of one at a time is some 0.5 us, two million of them a second
