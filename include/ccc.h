@@ -414,9 +414,9 @@ int ccc_check(int64_t rows, const int32_t *cu_seqlens, int32_t N,
  *               operand; rows after cu_seqlens[N] are not written.
  *  workspace    [dev] >= ccc_scan_workspace_size(..., 0) bytes, 256-byte
  *               aligned; need not be initialised.  Should a kernel ever give up
- *               one of its bounded internal waits (about half a second), it ends
- *               all the same, its results are undefined, and the workspace's first
- *               32-bit word is set to 1; the calls do not clear that word.
+ *               one of its bounded internal waits (ccc_wait_status), the
+ *               workspace's first 32-bit word is set to 1; the calls do not clear
+ *               that word.
  *
  * Backward: gradients of x, dt_raw, B and C in the inputs' types (zero for a
  * -1 request), and of A, D, dt_bias and the initial state in FP32, overwritten
@@ -535,7 +535,33 @@ int ccc_gated_norm_bwd(const void *y, int64_t rows, int32_t width, int64_t y_row
                        float *dweight, void *workspace, size_t workspace_bytes, void *cuda_stream);
 
 /*
- * The calls above with their arguments, in their order, as an array of 64-bit
+ * Bounded waits.  The kernels of ccc_scan_fwd, ccc_scan_bwd and ccc_ssm_update
+ * wait inside a CTA for copies and products that the same CTA has started.  No
+ * such wait should ever run out; each has a limit all the same, so that a
+ * mistake or a broken device ends a kernel instead of hanging it.  A kernel that
+ * gives a wait up waits for its copies and products in flight (a second at most),
+ * ends, and adds one to a counter on its device for each CTA that gave up.  Its
+ * results, and what later calls make of them, are then undefined: the caller
+ * discards them and the pools that they were written to.
+ *
+ * ccc_wait_status enqueues a copy of that counter, as it stands once the stream
+ * gets there, to status[0] [dev]: 0 while no wait has been given up on this
+ * device since the library was loaded.  The counter never falls; a caller that
+ * goes on after a failure compares with the value from before.
+ *
+ * ccc_set_wait_limit sets how many SM clocks a wait lasts at most, for the
+ * launches of the whole process from then on (a captured graph keeps what it was
+ * captured with); time in which the SM runs something else does not count.  0:
+ * a wait is given up at its first look that finds it unfinished, to test a
+ * caller's handling.
+ */
+#define CCC_WAIT_LIMIT_DEFAULT ((int64_t)1 << 30) /* about half a second */
+
+int ccc_wait_status(uint32_t *status, void *cuda_stream);
+int ccc_set_wait_limit(int64_t clocks);
+
+/*
+ * The mixer's calls with their arguments, in their order, as an array of 64-bit
  * integers (pointers as addresses, eps as the bits of its float): 33 of
  * ccc_scan_fwd, 41 of ccc_scan_bwd, 42 of ccc_scan_bwd_ex, 38 of ccc_ssm_update,
  * 14 and 21 of the norms.  For bindings whose cost grows with the number of arguments.

@@ -36,7 +36,9 @@ Around the convolution (``mixer.py``): the selective scan that reads its
 output (``selective_scan_fn`` / ``selective_scan_bwd`` / ``selective_scan``),
 the decode step of convolution and scan in one launch (``ssm_update``) and the
 gated RMS norm behind the scan (``gated_rms_norm_fn`` / ``gated_rms_norm_bwd``
-/ ``gated_rms_norm``).
+/ ``gated_rms_norm``).  ``given_up_waits`` tells whether a bounded wait inside
+the scan's and step's kernels ever ran out (``ccc_wait_status`` without the
+host read, ``set_wait_limit``).
 """
 from __future__ import annotations
 
@@ -58,7 +60,8 @@ __all__ = ["ccc_workspace_size", "ccc_fwd", "ccc_bwd", "ccc_bwd_noalloc", "ccc_u
            "CausalConv1dFn", "causal_conv1d", "CCCError", "library_path", "last_launch_count",
            "ccc_check", "check_metadata", "ccc_scan_workspace_size", "selective_scan_fn", "selective_scan_bwd",
            "selective_scan", "SelectiveScanFn", "ScanGrads", "ssm_update", "ccc_gated_norm_workspace_size",
-           "gated_rms_norm_fn", "gated_rms_norm_bwd", "gated_rms_norm", "GatedRMSNormFn"]
+           "gated_rms_norm_fn", "gated_rms_norm_bwd", "gated_rms_norm", "GatedRMSNormFn", "ccc_wait_status",
+           "given_up_waits", "set_wait_limit"]
 
 
 class CCCError(RuntimeError):
@@ -469,5 +472,5 @@ def causal_conv1d(x, weight, bias=None, cu_seqlens=None, conv_state=None, cache_
 
 
 from .mixer import (GatedRMSNormFn, ScanGrads, SelectiveScanFn, ccc_gated_norm_workspace_size,  # noqa: E402
-                    ccc_scan_workspace_size, gated_rms_norm, gated_rms_norm_bwd, gated_rms_norm_fn, selective_scan,
-                    selective_scan_bwd, selective_scan_fn, ssm_update)
+                    ccc_scan_workspace_size, ccc_wait_status, gated_rms_norm, gated_rms_norm_bwd, gated_rms_norm_fn,
+                    given_up_waits, selective_scan, selective_scan_bwd, selective_scan_fn, set_wait_limit, ssm_update)

@@ -18,11 +18,13 @@ EXPORTS = ("ccc_workspace_size", "ccc_fwd", "ccc_bwd", "ccc_fwd_ex", "ccc_bwd_ex
            "ccc_update", "ccc_update_ex", "ccc_check_status_words", "ccc_check", "ccc_status_string",
            "ccc_last_launch_count", "ccc_scan_workspace_size", "ccc_scan_fwd", "ccc_scan_bwd", "ccc_scan_bwd_ex",
            "ccc_ssm_update", "ccc_gated_norm_workspace_size", "ccc_gated_norm_fwd", "ccc_gated_norm_bwd",
-           "ccc_scan_fwd_v", "ccc_scan_bwd_v", "ccc_scan_bwd_ex_v", "ccc_ssm_update_v", "ccc_gated_norm_fwd_v", "ccc_gated_norm_bwd_v")
+           "ccc_wait_status", "ccc_set_wait_limit", "ccc_scan_fwd_v", "ccc_scan_bwd_v", "ccc_scan_bwd_ex_v", "ccc_ssm_update_v", "ccc_gated_norm_fwd_v", "ccc_gated_norm_bwd_v")
 
 # Launch option bits of ccc_fwd_ex / ccc_bwd_ex (include/ccc.h), and ccc_scan_bwd_ex's.
 OPT_OVERLAP_PROLOGUE = 1 << 0
 OPT_CARRY_EMPTY = 1 << 1
+# CCC_WAIT_LIMIT_DEFAULT
+WAIT_LIMIT_DEFAULT = 1 << 30
 
 # Size of the fixed scratch array behind ccc_bwd_noalloc (CCC_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -95,6 +97,10 @@ def lib() -> ctypes.CDLL:
             h.ccc_gated_norm_fwd.restype = ctypes.c_int
             h.ccc_gated_norm_bwd.argtypes = norm_in + [P, i64, P, i64, P, i64, P, P, sz, P]
             h.ccc_gated_norm_bwd.restype = ctypes.c_int
+            h.ccc_wait_status.argtypes = [P, P]
+            h.ccc_wait_status.restype = ctypes.c_int
+            h.ccc_set_wait_limit.argtypes = [i64]
+            h.ccc_set_wait_limit.restype = ctypes.c_int
             for name in ("ccc_scan_fwd", "ccc_scan_bwd", "ccc_scan_bwd_ex", "ccc_ssm_update", "ccc_gated_norm_fwd", "ccc_gated_norm_bwd"):
                 f = getattr(h, name + "_v")  # an array of int64 packed into bytes
                 f.argtypes, f.restype = [ctypes.c_char_p], ctypes.c_int

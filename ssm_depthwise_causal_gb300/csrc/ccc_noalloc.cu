@@ -28,12 +28,10 @@
 // is refused before any CUDA call.  Two calls whose work overlaps on the GPU
 // (different streams, or different host threads on the same device) race on
 // the array; callers must serialize them.
-#include <mutex>
-
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "ccc.h"
+#include "ccc_symbol.h"
 
 namespace {
 
@@ -41,78 +39,7 @@ constexpr size_t kScratchBytes = CCC_NOALLOC_SCRATCH_BYTES;
 
 static __device__ __align__(256) unsigned char g_scratch[kScratchBytes];
 
-// Driver entry points, fetched through the runtime so the library needs no
-// link against the driver library.
-using CtxGetCurrentFn = CUresult (*)(CUcontext *);
-using CtxGetIdFn = CUresult (*)(CUcontext, unsigned long long *);
-
-std::once_flag g_entry_once;
-CtxGetCurrentFn g_ctx_get_current = nullptr;
-CtxGetIdFn g_ctx_get_id = nullptr;
-
-void load_entry_points() {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-        g_ctx_get_current = reinterpret_cast<CtxGetCurrentFn>(f);
-    f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuCtxGetId", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-        g_ctx_get_id = reinterpret_cast<CtxGetIdFn>(f);
-}
-
-// Unique ID of the context current on this thread; 0 when there is none yet
-// (or it cannot be read).
-unsigned long long current_context_id() {
-    std::call_once(g_entry_once, load_entry_points);
-    if (!g_ctx_get_current || !g_ctx_get_id) return 0;
-    CUcontext ctx = nullptr;
-    if (g_ctx_get_current(&ctx) != CUDA_SUCCESS || ctx == nullptr) return 0;
-    unsigned long long id = 0;
-    if (g_ctx_get_id(ctx, &id) != CUDA_SUCCESS) return 0;
-    return id;
-}
-
-// Cache of looked-up addresses: context ID -> device address of g_scratch.
-struct Entry {
-    unsigned long long ctx_id;
-    void *addr;
-};
-constexpr int kCacheEntries = 64;
-std::mutex g_cache_mu;
-Entry g_cache[kCacheEntries] = {};
-int g_cache_next = 0;
-
-// Device address of g_scratch in the current context (looked up on the
-// first call in each context).
-int scratch_address(void **out) {
-    unsigned long long id = current_context_id();
-    if (id == 0) {
-        // No context on this thread yet: the lookup below makes the current
-        // device's primary context current (as any runtime call would).
-        void *p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_scratch) != cudaSuccess || p == nullptr) return CCC_ERR_CUDA;
-        id = current_context_id();
-        if (id == 0) {  // cannot key it: use the fresh lookup uncached
-            *out = p;
-            return CCC_OK;
-        }
-    }
-    std::lock_guard<std::mutex> lock(g_cache_mu);
-    for (const Entry &e : g_cache) {
-        if (e.ctx_id == id) {
-            *out = e.addr;
-            return CCC_OK;
-        }
-    }
-    void *p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_scratch) != cudaSuccess || p == nullptr) return CCC_ERR_CUDA;
-    g_cache[g_cache_next] = Entry{id, p};
-    g_cache_next = (g_cache_next + 1) % kCacheEntries;
-    *out = p;
-    return CCC_OK;
-}
+ccc::SymbolAddress g_address;
 
 }  // namespace
 
@@ -131,8 +58,8 @@ extern "C" int ccc_bwd_noalloc(const void *x, int64_t rows, int32_t C, int64_t x
     if (need > kScratchBytes) return CCC_ERR_WORKSPACE;
     void *ws = nullptr;
     if (need > 0) {
-        const int rc = scratch_address(&ws);
-        if (rc != CCC_OK) return rc;
+        ws = g_address.find(&g_scratch);
+        if (!ws) return CCC_ERR_CUDA;
     }
     return ccc_bwd(x, rows, C, x_row_stride, weight, w_dtype, width, bias, b_dtype, activation, saved_hist,
                    cu_seqlens, N,

@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const auto bar = [&](int b) { return base + kOffBar + 8 * b; };
-    volatile int *failed = reinterpret_cast<volatile int *>(smem + kOffBar + 8 * kBars);
-    const uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + kOffBar + 8 * kBars + 4);
+    WaitState *const wait = reinterpret_cast<WaitState *>(smem + kOffBar + 8 * kBars);
+    volatile int *failed = &wait->failed;
     Arrays *arrays = reinterpret_cast<Arrays *>(smem + kOffArr);
     if (tid == 0) {
         for (int b = 0; b < kSteps0; ++b) bar_init(bar(b), 1);
@@ -105,13 +105,13 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
         for (int b : {kSReady, kXReady, kClean}) bar_init(bar(b), 4);
         for (int b : {kYWritten0, kYWritten1}) bar_init(bar(b), 8);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        *failed = 0;
+        wait->failed = 0, wait->limit = a.waits.limit;
     }
-    if (warp == kMmaWarp) tmem_alloc(base + kOffBar + 8 * kBars + 4, 512);
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&wait->tmem), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    const uint32_t tmem = wait->tmem;
     grid_dependents_launch();
     if (warp != kTmaWarp) grid_dependency_wait();  // (that warp looks for its chunks first)
     const auto desc = [&](int k) -> const Desc & {
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_free(tmem, 512);
-    if (tid == 0 && *failed) *a.status = 1;
+    if (tid == 0 && *failed) *a.status = 1, report_given_up(a.waits);
 }
 
 }  // namespace
@@ -638,6 +638,7 @@ cudaError_t launch_scan_tc_fwd(const ScanArgs &s, const ScanTcPlan &plan, unsign
     a.s = s;
     a.pairs = plan.pairs, a.pairs_per_group = plan.pairs_per_group, a.tiles = plan.tiles;
     a.status = reinterpret_cast<int *>(ws + plan.status);
+    a.waits = current_waits();
     a.local = reinterpret_cast<float *>(ws + plan.local);
     a.keep = reinterpret_cast<float *>(ws + plan.keep);
     a.flag = reinterpret_cast<int *>(ws + plan.flag);

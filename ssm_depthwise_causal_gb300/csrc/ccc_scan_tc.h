@@ -4,6 +4,7 @@
 #include <cuda.h>
 
 #include "ccc_scan.h"
+#include "ccc_waits.h"
 
 namespace ccc {
 
@@ -18,6 +19,7 @@ struct ScanTcArgs {
     float *staged;     // [parts][128][NW]: the slot's state that an open sequence started from
     uint16_t *store;   // [chunk][pair][three parts][128][NW]
     int *status;       // set to 1 when a wait was given up
+    Waits waits;
 };
 
 // How a call is divided; a function of the host arguments alone.

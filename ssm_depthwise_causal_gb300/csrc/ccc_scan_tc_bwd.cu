@@ -90,6 +90,7 @@ struct BwdTcArgs {
     const uint16_t *states;  // reverse: the states before the chunks
     float *sums;             // [chunk][head tile][kPlanes][128]
     int *status;
+    Waits waits;
 };
 
 // Planes of `sums`, the sums of T1 T2 L over a row: within the diagonal block
@@ -112,8 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const auto bar = [&](int b) { return base + kOffBar + 8 * b; };
-    volatile int *failed = reinterpret_cast<volatile int *>(smem + kOffBar + 8 * kBars);
-    const uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + kOffBar + 8 * kBars + 4);
+    WaitState *const wait = reinterpret_cast<WaitState *>(smem + kOffBar + 8 * kBars);
+    volatile int *failed = &wait->failed;
     Arrays &r = *reinterpret_cast<Arrays *>(smem + kOffArr);
     const int rep = a.s.H / a.s.G * a.tiles;  // head tiles of a group
     if (tid == 0) {
@@ -121,13 +122,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             bar_init(bar(b), b == kArrays ? 16 : b == kEmptyQK ? 17 : 1);
         for (int b = kWReady; b < kBars; ++b) bar_init(bar(b), 16);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        *failed = 0;
+        wait->failed = 0, wait->limit = a.waits.limit;
     }
-    if (warp == kMmaWarp) tmem_alloc(base + kOffBar + 8 * kBars + 4, 512);
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&wait->tmem), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    const uint32_t tmem = wait->tmem;
     grid_dependents_launch();
     grid_dependency_wait();
     const auto desc = [&](int k) -> const Desc & {
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_free(tmem, 512);
-    if (tid == 0 && *failed) *a.status = 1;
+    if (tid == 0 && *failed) *a.status = 1, report_given_up(a.waits);
 }
 
 // ddt of a chunk and head, and its share of dA, dD, ddt_bias, from the sums: a thread per token.
@@ -721,6 +722,7 @@ cudaError_t launch_scan_tc_bwd(const ScanArgs &s, const ScanTcBwdPlan &plan, uns
     a.slots = plan.slots;
     a.sums = reinterpret_cast<float *>(ws + plan.sums);
     a.status = reinterpret_cast<int *>(ws + plan.walk.status);
+    a.waits = current_waits();
     const int nw = 64 * plan.walk.nb;
     const int64_t store_rows = plan.slots * plan.walk.pairs * 3 * Q;
     CUtensorMap x, dy, b, c, es, eg;

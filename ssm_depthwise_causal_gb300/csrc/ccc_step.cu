@@ -54,6 +54,7 @@ struct StepArgs {
     const int32_t *accepted;
     int heads_per_cta, ctas;  // of a group
     int state_at;             // where the state begins in shared memory, in floats
+    Waits waits;
 };
 
 __device__ __forceinline__ float silu1(float z) {
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
     namespace cg = cooperative_groups;
     extern __shared__ __align__(128) float smem[];
     __shared__ uint64_t s_full[kStages];
-    __shared__ int s_failed;
+    __shared__ WaitState s_wait;
     constexpr int kRows = 8 / NV;                       // rows of a lane in a piece
     constexpr int kPiece = kWarps * (32 / LR) * kRows;  // rows of a piece: up to 32 KB
     const ScanArgs &s = a.s;
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
     };
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) bar_init(smem_addr(&s_full[i]), 1);
-        s_failed = 0;
+        s_wait.failed = 0, s_wait.limit = a.waits.limit;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         for (int i = 0; i < min(kStages, pieces); ++i) load(i);
     }
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
                 __syncthreads();
             }
             if (i >= pieces) continue;
-            if (t0 == 0) bar_wait(smem_addr(&s_full[i % kStages]), (i / kStages) & 1, &s_failed);
+            if (t0 == 0) bar_wait(smem_addr(&s_full[i % kStages]), (i / kStages) & 1, &s_wait.failed);
             for (int j = 0; j < nt; ++j) {
                 const float *bj = bcs + j * bc, *xj = xs + j * xw;
                 const bool kept = t0 + j < a.held, last = t0 + j + 1 == len;
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
         }
     }
     if (a.ctas > 1) cg::this_cluster().sync();  // the others have fetched this CTA's share
+    if (tid == 0 && s_wait.failed) report_given_up(a.waits);
 }
 
 template <int LR, int NV>
@@ -348,6 +350,7 @@ extern "C" int ccc_ssm_update(const void *xBC, int64_t rows, int32_t H, int32_t 
     a.conv = static_cast<uint16_t *>(conv_state), a.state_len = state_len, a.st_slot = st_slot, a.st_c = st_c, a.st_l = st_l;
     a.held = ssm_len, a.st_pos = ssm_st_pos, a.accepted = num_accepted;
     const int rep = H / G;
+    a.waits = current_waits();
     a.heads_per_cta = step_heads(static_cast<int64_t>(N) * G, rep, P, N_state);
     while (a.heads_per_cta > 1 && staged_bytes(a.heads_per_cta, P, N_state) > 48 * 1024) a.heads_per_cta = (a.heads_per_cta + 1) / 2;
     a.heads_per_cta = std::max(a.heads_per_cta, (rep + 7) / 8);

@@ -7,6 +7,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "ccc_waits.h"
+
 namespace ccc {
 
 // ------------------------------------------------------------- mbarriers --
@@ -35,14 +37,28 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Waits until the barrier's phase `parity` is over.  Gives up after about half a
-// second of SM clocks, or at once when another wait of the CTA has given up
-// (*failed, in shared memory): the caller then leaves its loop.
+// What the waits of a CTA share, in shared memory.
+struct WaitState {
+    int failed;       // a wait has been given up
+    uint32_t tmem;    // (where tcgen05.alloc leaves its address)
+    long long limit;  // clocks that a wait lasts at most
+};
+
+// Waits until the barrier's phase `parity` is over.  Gives up after the limit
+// in SM clocks, or at once when another wait of the CTA has given up (*failed):
+// the caller then leaves its loop.  From one look at the barrier to the next at
+// most kGap clocks count, so that the time in which the SM runs something else
+// does not.  `failed` is the first member of a WaitState.
 // (The loop is not inlined: a kernel has dozens of waits.)
 static __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int *failed) {
-    const long long t0 = clock64();
+    constexpr long long kGap = 1ll << 22;
+    const long long limit = reinterpret_cast<volatile WaitState *>(failed)->limit;
+    long long last = clock64(), waited = 0;
     while (!bar_try(bar, parity)) {
-        if (*failed || clock64() - t0 > (1ll << 30)) {
+        const long long now = clock64();
+        waited += min(max(now - last, 0ll), kGap);
+        last = now;
+        if (*failed || waited > limit) {
             *failed = 1;
             return false;
         }
@@ -52,6 +68,11 @@ static __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity,
 
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *failed) {
     return bar_try(bar, parity) || bar_wait_long(bar, parity, failed);
+}
+
+// A CTA that gave up a wait says so, at its end.
+__device__ __forceinline__ void report_given_up(const Waits &w) {
+    if (w.given_up) atomicAdd(w.given_up, 1u);
 }
 
 // Generic-proxy writes to shared memory become visible to TMA and tcgen05.

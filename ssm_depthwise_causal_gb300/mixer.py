@@ -22,7 +22,7 @@ from . import CCCError, _act_code, _lib, _on_current_device, _pool_args, _stream
 
 __all__ = ["ScanGrads", "SelectiveScanFn", "GatedRMSNormFn", "ccc_scan_workspace_size", "ccc_gated_norm_workspace_size",
            "selective_scan_fn", "selective_scan_bwd", "selective_scan", "ssm_update", "gated_rms_norm_fn",
-           "gated_rms_norm_bwd", "gated_rms_norm"]
+           "gated_rms_norm_bwd", "gated_rms_norm", "ccc_wait_status", "given_up_waits", "set_wait_limit"]
 
 
 class ScanGrads(NamedTuple):
@@ -452,3 +452,32 @@ class GatedRMSNormFn(torch.autograd.Function):
 def gated_rms_norm(y, z, weight, *, eps=1e-5, group_size=None, norm_before_gate=False) -> torch.Tensor:
     """Differentiable gated RMS norm (see GatedRMSNormFn)."""
     return GatedRMSNormFn.apply(y, z, weight, eps, group_size, norm_before_gate)
+
+
+def ccc_wait_status(status=None, stream=None) -> torch.Tensor:
+    """How many CTAs have given up a bounded wait on the current device (include/ccc.h, ccc_wait_status): an int32 tensor whose
+    first element receives the count once the stream gets there (no synchronization here).  Anything but 0: results of the
+    scans and decode steps since it was 0 are undefined."""
+    if status is None:
+        status = _under_stream(torch.empty)(1, dtype=torch.int32, device="cuda", stream=stream)
+    if status.dtype is not torch.int32 or status.numel() < 1 or not status.is_contiguous():
+        raise ValueError("status must be a contiguous int32 tensor")
+    _on_current_device(status)
+    rc = _lib.lib().ccc_wait_status(status.data_ptr(), _stream(stream))
+    if rc != 0:
+        raise CCCError(rc, "ccc_wait_status")
+    return status
+
+
+def given_up_waits() -> int:
+    """ccc_wait_status, then a host read (synchronizes the current stream): 0 unless a scan or decode step on this device gave
+    a wait up."""
+    return int(ccc_wait_status()[0].item()) & 0xffffffff
+
+
+def set_wait_limit(clocks=None) -> None:
+    """How many SM clocks a wait inside a scan or decode step lasts at most, from the next launch on (ccc_set_wait_limit);
+    None: the default, about half a second."""
+    rc = _lib.lib().ccc_set_wait_limit(_lib.WAIT_LIMIT_DEFAULT if clocks is None else int(clocks))
+    if rc != 0:
+        raise CCCError(rc, "ccc_set_wait_limit")

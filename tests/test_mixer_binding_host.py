@@ -126,3 +126,19 @@ def test_several_tokens_need_positions():
                  step(ssm_state=flat[:, None], xBC=b16(6, 768), dt=torch.zeros(6, 4)), step(xBC=b16(3, 2, 768), dt=torch.zeros(3, 2, 4), cu_seqlens=None)):
         with pytest.raises(ValueError, match="CUDA tensors"):
             ccc.ssm_update(**good)
+
+
+def test_wait_limit_and_status_refuse():
+    from ssm_depthwise_causal_gb300 import _build, _lib
+    from tests.test_host import E_ALIGN, E_NULL, E_SHAPE
+    _build.build()
+    assert _lib.lib().ccc_set_wait_limit(-1) == E_SHAPE and _lib.lib().ccc_set_wait_limit(0) == 0
+    ccc.set_wait_limit()  # the default again
+    assert _lib.lib().ccc_wait_status(None, None) == E_NULL and _lib.lib().ccc_wait_status(4098, None) == E_ALIGN
+    with pytest.raises(ccc.CCCError):
+        ccc.set_wait_limit(-5)
+    for bad in (ints(0), ints(1, torch.int64)):
+        with pytest.raises(ValueError, match="status must"):
+            ccc.ccc_wait_status(bad)
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        ccc.ccc_wait_status(ints(1))
