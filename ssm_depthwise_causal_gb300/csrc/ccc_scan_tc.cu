@@ -67,7 +67,6 @@ constexpr int kDescs = 8, kAhead = 3;  // published ahead of the loads; a slot i
 constexpr uint32_t kOffDesc = kOffArr + 2 * sizeof(Arrays);
 constexpr uint32_t kOffBar = kOffDesc + kDescs * sizeof(Desc);
 constexpr uint32_t kSmem = kOffBar + 512;
-static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 constexpr uint32_t kColM = 0, kColY = 128, kColX = 256, kColS = 384;
 
@@ -83,6 +82,7 @@ enum Bar {
     kYWritten0, kYWritten1,                           // a head's y lies in shared memory
     kBars
 };
+static_assert(kSmem <= 232448 && 8 * kBars + sizeof(WaitState) <= 512, "shared memory of a CTA");
 
 // NB: tiles of 64 state values.
 template <int NB>
@@ -140,30 +140,33 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
             wk.next(a.s);
         };
         for (int i = 0; i < kAhead; ++i) publish();
-        int k = 0;
+        int k = 0, loaded_k = 0, loaded_c = 0, loaded_v = 0;
         for (;;) {
             const int st = k & 1;
             const Desc &d = reinterpret_cast<const Desc *>(smem + kOffDesc)[k % kDescs];
             const int row = d.row, pair = d.pair;
-            if (!(d.flags & kMore)) break;
+            if (__any_sync(kFull, *failed || !(d.flags & kMore))) break;
             const uint32_t free = ((k >> 1) & 1) ^ 1;
             publish();  // well ahead of the loads: the steps start from it
             if (lane == 0) {
                 const int g = pair / a.pairs_per_group;
                 bar_wait(bar(kEmptyK0 + st), free, failed);
                 if (!*failed) {
+                    ++loaded_k;
                     bar_expect(bar(kFullK0 + st), NB * kTile);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) tma_load(base + kOffK + (2 * st + b) * kTile, &a.mk, bar(kFullK0 + st), b * 64, g, row);
                 }
                 bar_wait(bar(kEmptyC), (k & 1) ^ 1, failed);
                 if (!*failed) {
+                    ++loaded_c;
                     bar_expect(bar(kFullC), NB * kTile);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) tma_load(base + kOffC + b * kTile, &a.mc, bar(kFullC), b * 64, g, row);
                 }
                 bar_wait(bar(kEmptyV0 + st), free, failed);
                 if (!*failed) {
+                    ++loaded_v;
                     bar_expect(bar(kFullV0 + st), 2 * kTile);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -175,12 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
             __syncwarp();
             ++k;
         }
-        if (lane == 0 && *failed) {  // given up: no copy may be in flight when the CTA ends
-            const long long t0 = clock64();
-            for (int i = max(0, k - 2); i < k; ++i)
-                while (!(bar_try(bar(kFullK0 + (i & 1)), (i >> 1) & 1) && bar_try(bar(kFullV0 + (i & 1)), (i >> 1) & 1)) && clock64() - t0 < (1ll << 31)) {}
-            while (k > 0 && !bar_try(bar(kFullC), (k - 1) & 1) && clock64() - t0 < (1ll << 31)) {}
-        }
+        if (lane == 0) wait->started[0] = loaded_k, wait->started[1] = loaded_c, wait->started[2] = loaded_v;
     } else if (warp == kMmaWarp) {  // -------------------------------- products
         int k = 0;
         for (;; ++k) {
@@ -237,11 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
             }
             __syncwarp();
         }
-        if (*failed && k > 0) {  // given up: let the products in flight end
-            const long long t0 = clock64();
-            while (!bar_try(bar(kYFull), (k - 1) & 1) && clock64() - t0 < (1ll << 31)) {}
-        }
-        __syncwarp();
+        if (lane == 0) wait->started[3] = k;
     } else if (warp >= kStepWarp) {  // ---------------------- steps and decays
         const int hd = warp - kStepWarp;
         int pair = -1, ahead_pair = -1;
@@ -250,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
         uint32_t raw[4], next[4];
         const auto fetch = [&](int k, uint32_t (&to)[4]) {  // false past the last chunk
             const Desc &d = desc(k);
-            if (*failed || !(d.flags & kMore)) return false;
+            if (__any_sync(kFull, *failed || !(d.flags & kMore))) return false;
             if (d.pair != ahead_pair) {
                 ahead_pair = d.pair;
                 ahead = head_of(a, ahead_pair, hd);
@@ -303,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
         float D = 0.0f;
         for (int k = 0;; ++k) {
             const Desc &d = desc(k);
-            if (*failed || !(d.flags & kMore)) break;
+            if (__any_sync(kFull, *failed || !(d.flags & kMore))) break;
             const int st = k & 1, len = d.len, row = d.row;
             const uint32_t parity = k & 1;
             const bool zero = d.flags & kDead;
@@ -438,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
         Head state{};
         while (true) {
             const Desc &d = desc(k);
-            const bool more = !*failed && (d.flags & kMore);
+            const bool more = !__any_sync(kFull, *failed || !(d.flags & kMore));
             if (k > 0) {
                 bar_wait(bar(kDsFull), (k - 1) & 1, failed);
                 tc_fence_after();
@@ -514,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
         int clean = 0;
         for (int k = 0;; ++k) {
             const Desc &d = desc(k);
-            if (*failed || !(d.flags & kMore)) break;
+            if (__any_sync(kFull, *failed || !(d.flags & kMore))) break;
             const int st = k & 1, len = d.len;
             const uint32_t ring = (k >> 1) & 1;
             bar_wait(bar(kFullV0 + st), ring, failed);
@@ -569,6 +563,15 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
     }
     tc_fence_before();
     __syncthreads();
+    if (*failed) {
+        if (tid == 0) {
+            bar_drain(bar(kFullK0), 2, wait->started[0]);
+            bar_drain(bar(kFullC), 1, wait->started[1]);
+            bar_drain(bar(kFullV0), 2, wait->started[2]);
+            bar_drain(bar(kYFull), 1, wait->started[3]);
+        }
+        __syncthreads();
+    }
     tc_fence_after();
     if (warp == kMmaWarp) tmem_free(tmem, 512);
     if (tid == 0 && *failed) *a.status = 1, report_given_up(a.waits);

@@ -66,7 +66,6 @@ constexpr int kDescs = 4;
 constexpr uint32_t kOffDesc = kOffArr + sizeof(Arrays);
 constexpr uint32_t kOffBar = kOffDesc + kDescs * sizeof(Desc);
 constexpr uint32_t kSmem = kOffBar + 512;
-static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 constexpr uint32_t kColT1 = 0, kColW = 128, kColAcc = 256, kColE = 384;
 
@@ -81,6 +80,7 @@ enum Bar {
     kDxWritten0, kDxWritten1,
     kBars
 };
+static_assert(kSmem <= 232448 && 8 * kBars + sizeof(WaitState) <= 512, "shared memory of a CTA");
 
 struct BwdTcArgs {
     CUtensorMap mq, mk, mu, mv, me, mdx;  // rows' and columns' sides, states (boxes of 64 rows), dx
@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 
     if (warp == kTmaWarp) {  // ------------------------------- tasks and loads
         if (lane == 0) {
-            int task = 0, k = 0;  // tasks published, heads loaded
+            int task = 0, k = 0;  // tasks published, heads gone through
+            int loaded_qk = 0, loaded_u = 0;
             const auto publish = [&](int64_t &at) {  // the next chunk and group that exist; false after the last
                 Desc &d = reinterpret_cast<Desc *>(smem + kOffDesc)[task % kDescs];
                 d.flags = 0;
@@ -166,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     if (*failed) continue;
                     const uint32_t to = base + kOffU + st * kHead, full = bar(kFullU0 + st);
                     const int h = d.g * (a.s.H / a.s.G) + v / a.tiles, tile = v % a.tiles;
+                    ++loaded_u;
                     bar_expect(full, 2 * kTile + 3 * NB * (kTile / 2));
                     tma_load(to, &a.mu, full, tile * 64, h, d.row);
                     tma_load(to + kTile, &a.mv, full, tile * 64, h, d.row);
@@ -184,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     if (v == 0) {
                         bar_wait(bar(kEmptyQK), (t & 1) ^ 1, failed);
                         if (!*failed) {
+                            ++loaded_qk;
                             bar_expect(bar(kFullQK), 2 * NB * kTile);
 #pragma unroll
                             for (int b = 0; b < NB; ++b) {
@@ -201,10 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 }
                 if (*failed) break;
             }
-            if (*failed) {  // given up: no copy may be in flight when the CTA ends
-                const long long t0 = clock64();
-                while (clock64() - t0 < (1ll << 22)) {}
-            }
+            wait->started[0] = loaded_u, wait->started[1] = loaded_qk;
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {  // -------------------------------- products
@@ -281,11 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 __syncwarp();
             }
         }
-        if (*failed) {  // given up: let the products in flight end
-            const long long t0 = clock64();
-            while (clock64() - t0 < (1ll << 22)) {}
-        }
-        __syncwarp();
+        if (lane == 0) wait->started[2] = k;
     } else if (warp == kStepWarp) {  // ------------------- steps and decays
         struct Raw {
             uint32_t A, bias, dt[4];  // as loaded
@@ -295,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const auto fetch = [&](Raw &to) {
             const Desc &d = desc(ft);
             to.len = -1;
-            if (*failed || !(d.flags & kMore)) return;
+            if (__any_sync(kFull, *failed || !(d.flags & kMore))) return;
             const int h = d.g * (a.s.H / a.s.G) + fv / a.tiles;
             to.len = d.len;
             to.A = par_bits(a.s.A, a.s.p_bf16, h);
@@ -337,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             }
             if (lane < 4) r.total[lane] = lane == 0 ? P[0] : lane == 1 ? P[1] : lane == 2 ? P[2] : P[3];
             warp_arrive(bar(kSteps));
-            if (*failed) break;
+            if (__any_sync(kFull, *failed)) break;
             now = next;  // (waits for its loads)
             if (now.len >= 0) fetch(next);
         }
@@ -367,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         int k = 0;
         for (int t = 0;; ++t) {
             const Desc &d = desc(t);
-            if (*failed || !(d.flags & kMore)) break;
+            if (__any_sync(kFull, *failed || !(d.flags & kMore))) break;
             const int len = d.len;
             const bool whole = len == Q, dead = d.flags & kDead;
             float2 out[NB * 8];  // sum over the heads of s_i (U E)_i
@@ -593,6 +589,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
+    if (*failed) {
+        if (tid == 0) {
+            bar_drain(bar(kFullU0), 2, wait->started[0]);
+            bar_drain(bar(kFullQK), 1, wait->started[1]);
+            bar_drain(bar(kWUsed), 1, wait->started[2]);
+        }
+        __syncthreads();
+    }
     tc_fence_after();
     if (warp == kMmaWarp) tmem_free(tmem, 512);
     if (tid == 0 && *failed) *a.status = 1, report_given_up(a.waits);

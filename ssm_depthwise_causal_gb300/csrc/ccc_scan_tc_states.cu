@@ -41,7 +41,6 @@ constexpr int kDescs = 8, kAhead = 3;  // published ahead of the loads; a slot i
 constexpr uint32_t kOffDesc = kOffArr + 2 * sizeof(Arrays);
 constexpr uint32_t kOffBar = kOffDesc + kDescs * sizeof(Desc);
 constexpr uint32_t kSmem = kOffBar + 512;
-static_assert(kSmem <= 232448, "shared memory of a CTA");
 constexpr uint32_t kColX = 0, kColsX = 192, kColD = 384;  // w v twice; the products
 
 // A waiter looks at a phase's parity alone: never two phases late, nor one early (ccc_scan_tc.cu).
@@ -52,6 +51,7 @@ enum Bar {
     kSteps0, kSteps1, kArrays0, kArrays1,
     kBars
 };
+static_assert(kSmem <= 232448 && 8 * kBars + sizeof(WaitState) <= 512, "shared memory of a CTA");
 
 template <int NB, bool REV, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1) states_kernel(const __grid_constant__ ScanTcArgs a) {
@@ -113,17 +113,18 @@ __global__ void __launch_bounds__(kThreads, 1) states_kernel(const __grid_consta
                 wk.next(a.s);
             };
             for (int i = 0; i < kAhead; ++i) publish();
-            int k = 0;
+            int k = 0, loaded_k = 0, loaded_v = 0;
             for (;;) {
                 const int st = k & 1;
                 const Desc &d = reinterpret_cast<const Desc *>(smem + kOffDesc)[k % kDescs];
                 const int row = d.row, pair = d.pair;
-                if (!(d.flags & kMore)) break;
+                if (__any_sync(kFull, *failed || !(d.flags & kMore))) break;
                 const uint32_t free = ((k >> 1) & 1) ^ 1;
                 publish();  // well ahead of the loads: the steps start from it
                 if (lane == 0) {
                     bar_wait(bar(kEmptyV0 + st), free, failed);
                     if (!*failed) {
+                        ++loaded_v;
                         bar_expect(bar(kFullV0 + st), 2 * kTile);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) states_kernel(const __grid_consta
                     }
                     bar_wait(bar(kEmptyK0 + st), free, failed);
                     if (!*failed) {
+                        ++loaded_k;
                         bar_expect(bar(kFullK0 + st), NB * kTile);
 #pragma unroll
                         for (int b = 0; b < NB; ++b)
@@ -142,12 +144,10 @@ __global__ void __launch_bounds__(kThreads, 1) states_kernel(const __grid_consta
                 __syncwarp();
                 ++k;
             }
-            if (lane == 0 && *failed) {  // given up: no copy may be in flight when the CTA ends
-                const long long t0 = clock64();
-                while (clock64() - t0 < (1ll << 22)) {}
-            }
+            if (lane == 0) wait->started[0] = loaded_k, wait->started[1] = loaded_v;
         } else if (warp == kMmaWarp) {  // ---------------------------- products
-            for (int k = 0;; ++k) {
+            int k = 0;
+            for (;; ++k) {
                 const Desc &d = desc(k);
                 if (__any_sync(kFull, *failed || !(d.flags & kMore))) break;
                 const int st = k & 1;
@@ -167,11 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) states_kernel(const __grid_consta
                 }
                 __syncwarp();
             }
-            if (*failed) {  // given up: let the products in flight end
-                const long long t0 = clock64();
-                while (clock64() - t0 < (1ll << 22)) {}
-            }
-            __syncwarp();
+            if (lane == 0) wait->started[2] = k;
         } else {  // ------------------------------------------ steps and decays
             const int hd = warp - kStepWarp;
             int pair = -1, ahead_pair = -1;
@@ -180,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) states_kernel(const __grid_consta
             uint32_t raw[4], next[4];
             const auto fetch = [&](int k, uint32_t (&to)[4]) {  // false past the last chunk
                 const Desc &d = desc(k);
-                if (*failed || !(d.flags & kMore)) return false;
+                if (__any_sync(kFull, *failed || !(d.flags & kMore))) return false;
                 if (d.pair != ahead_pair) {
                     ahead_pair = d.pair;
                     ahead = head_of(a, ahead_pair, hd);
@@ -225,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) states_kernel(const __grid_consta
         int clean = 0;
         for (int k = 0;; ++k) {
             const Desc &d = desc(k);
-            if (*failed || !(d.flags & kMore)) break;
+            if (__any_sync(kFull, *failed || !(d.flags & kMore))) break;
             const int st = k & 1, len = d.len;
             const uint32_t ring = (k >> 1) & 1;
             bar_wait(bar(kFullV0 + st), ring, failed);
@@ -292,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) states_kernel(const __grid_consta
         Head state{};
         for (int k = 0;; ++k) {
             const Desc &d = desc(k);
-            if (*failed || !(d.flags & kMore)) break;
+            if (__any_sync(kFull, *failed || !(d.flags & kMore))) break;
             const int st = k & 1, flags = d.flags, n = d.n;
             const uint32_t ring = (k >> 1) & 1;
             const int64_t place = (static_cast<int64_t>(d.row) / Q + n) * a.pairs + d.pair;
@@ -396,6 +392,14 @@ __global__ void __launch_bounds__(kThreads, 1) states_kernel(const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
+    if (*failed) {
+        if (tid == 0) {
+            bar_drain(bar(kFullK0), 2, wait->started[0]);
+            bar_drain(bar(kFullV0), 2, wait->started[1]);
+            bar_drain(bar(kEmptyK0), 2, wait->started[2]);
+        }
+        __syncthreads();
+    }
     tc_fence_after();
     if (warp == kMmaWarp) tmem_free(tmem, 512);
     if (tid == 0 && *failed) *a.status = 1, report_given_up(a.waits);

@@ -42,6 +42,7 @@ struct WaitState {
     int failed;       // a wait has been given up
     uint32_t tmem;    // (where tcgen05.alloc leaves its address)
     long long limit;  // clocks that a wait lasts at most
+    int started[4];   // copies and products that the CTA has started, kind by kind (bar_drain)
 };
 
 // Waits until the barrier's phase `parity` is over.  Gives up after the limit
@@ -68,6 +69,16 @@ static __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity,
 
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *failed) {
     return bar_try(bar, parity) || bar_wait_long(bar, parity, failed);
+}
+
+// Where a CTA gave a wait up, before it may end: until the last phases of `stages` barriers side by side, for which copies or
+// products number 0 .. n - 1 were started in turn, are over (2^31 clocks, a second, at most).  n has to count what was
+// started alone: the parity of a later phase would pass for done.  Called when every warp has left its loop, since a wait can
+// run out after the warp that started what it waits for has gone through.
+__device__ __forceinline__ void bar_drain(uint32_t bar, int stages, int n) {
+    const long long t0 = clock64();
+    for (int i = max(0, n - stages); i < n; ++i)
+        while (!bar_try(bar + i % stages * 8, (i / stages) & 1) && clock64() - t0 < (1ll << 31)) {}
 }
 
 // A CTA that gave up a wait says so, at its end.

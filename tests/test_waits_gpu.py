@@ -77,3 +77,36 @@ assert all(torch.equal(a, b) for a, b in zip(made, want))
 assert ccc.given_up_waits() == 0
 """
     subprocess.run([sys.executable, "-c", code], check=True, timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+@pytest.fixture
+def no_patience():
+    """Waits are given up at the first look that finds them unfinished."""
+    ccc.set_wait_limit(0)
+    yield
+    ccc.set_wait_limit()
+
+
+@pytest.mark.parametrize("name", ["forward", "backward"])
+def test_scan_waits_run_out(name, no_patience):
+    """The kernels end, soon, and say so; the device, and the next call with patience, are as before."""
+    calls = Calls(seed=82)
+    ccc.set_wait_limit()
+    run = getattr(calls, name)
+    want = [t.clone() for t in run()]
+    words = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    before = ccc.given_up_waits()
+    for _ in range(3):
+        ccc.set_wait_limit(0)
+        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        begin.record()
+        run(workspace=words)
+        end.record()
+        ccc.set_wait_limit()
+        count = ccc.given_up_waits()
+        assert count > before and int(words[:4].view(torch.int32)) == 1
+        # a drain that waits for what was never started takes a second
+        assert begin.elapsed_time(end) < 100.0
+        before = count
+        assert all(torch.equal(a, b) for a, b in zip(want, run()))
+        assert ccc.given_up_waits() == before
