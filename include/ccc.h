@@ -542,7 +542,8 @@ int ccc_gated_norm_bwd(const void *y, int64_t rows, int32_t width, int64_t y_row
  * gives a wait up waits for its copies and products in flight (a second at most),
  * ends, and adds one to a counter on its device for each CTA that gave up.  Its
  * results, and what later calls make of them, are then undefined: the caller
- * discards them and the pools that they were written to.
+ * discards them and the pools that they were written to.  (A decode step stores
+ * no state that it has not waited for.)
  *
  * ccc_wait_status enqueues a copy of that counter, as it stands once the stream
  * gets there, to status[0] [dev]: 0 while no wait has been given up on this

@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
     // B and C come first: their place is the same in every CTA
     float *bcs = smem, *xs = bcs + kTokens * bc, *ys = xs + kTokens * xw, *s_dt = ys + kTokens * xw, *s_decay = s_dt + kTokens * hc;
     float *state = smem + a.state_at;
+    volatile int *const failed = &s_wait.failed;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const Seq seq = scan_seq(s, n);
     const int len = static_cast<int>(seq.end - seq.begin);
@@ -110,6 +111,11 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
     const int keep = min(len + a.width - 2, a.state_len);
 
     const int col = lane % LR * 4, sub = lane / LR;
+    int started = min(kStages, pieces);  // copies (thread 0's count)
+    // A warp whose wait ran out has no state: it stores none any more, and waits no more (a phase too far ahead would pass for
+    // done).  Its rows of y are undefined.  (Leaving them unwritten as well, by a look at the CTA's flag behind each piece, cost
+    // the 256-request step 2 of 293 us.)
+    bool here = true;
     for (int i = 0; i < rounds; ++i) {
         const int base = i * kPiece;
         float *piece = state + i % kStages * kPiece * s.N;
@@ -171,8 +177,11 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
                 __syncthreads();
             }
             if (i >= pieces) continue;
-            if (t0 == 0) bar_wait(smem_addr(&s_full[i % kStages]), (i / kStages) & 1, &s_wait.failed);
-            for (int j = 0; j < nt; ++j) {
+            if (t0 == 0) {
+                const uint32_t bar = smem_addr(&s_full[i % kStages]), parity = (i / kStages) & 1;
+                here = here && __all_sync(kFull, a.waits.limit > 0 ? bar_wait(bar, parity, failed) : bar_look(bar, parity, failed));
+            }
+            for (int j = 0; here && j < nt; ++j) {
                 const float *bj = bcs + j * bc, *xj = xs + j * xw;
                 const bool kept = t0 + j < a.held, last = t0 + j + 1 == len;
                 float4 bv[NV], cv[NV];
@@ -230,9 +239,10 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
                 }
             }
             __syncthreads();
-            if (t0 + kTokens >= len && tid == 0 && i + kStages < pieces) {
+            if (t0 + kTokens >= len && tid == 0 && i + kStages < pieces && here) {
                 fence_async();  // the piece has been read (and written): a copy may follow
                 load(i + kStages);
+                ++started;
             }
             const int wide = min(base + kPiece, xw) - base;
             for (int e = tid; e < nt * wide; e += kThreads) {
@@ -242,7 +252,10 @@ __global__ void __launch_bounds__(kThreads, 3) step_kernel(const StepArgs a) {
         }
     }
     if (a.ctas > 1) cg::this_cluster().sync();  // the others have fetched this CTA's share
-    if (tid == 0 && s_wait.failed) report_given_up(a.waits);
+    if (tid == 0 && *failed) {
+        bar_drain(smem_addr(&s_full[0]), kStages, started);  // no copy may be in flight when the CTA ends
+        report_given_up(a.waits);
+    }
 }
 
 template <int LR, int NV>

@@ -71,6 +71,20 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return bar_try(bar, parity) || bar_wait_long(bar, parity, failed);
 }
 
+// The same with no patience at all: bar_try lets the hardware wait a little, longer than a copy takes.
+__device__ __forceinline__ bool bar_look(uint32_t bar, uint32_t parity, volatile int *failed) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (!ok) *failed = 1;
+    return ok != 0;
+}
+
 // Where a CTA gave a wait up, before it may end: until the last phases of `stages` barriers side by side, for which copies or
 // products number 0 .. n - 1 were started in turn, are over (2^31 clocks, a second, at most).  n has to count what was
 // started alone: the parity of a later phase would pass for done.  Called when every warp has left its loop, since a wait can

@@ -35,9 +35,9 @@ class Calls:
         return tuple(ccc.selective_scan_bwd(g.x, g.dt, g.A, g.B, g.C, g.dy, g.cu, initial_state=g.initial, d_final_state=g.d_final, want_d_initial=True,
                                             **self.par, **kw))
 
-    def step(self, conv=None, pool=None, out=None):
+    def step(self, conv=None, pool=None):
         conv, pool = self.conv.clone() if conv is None else conv, self.pool.clone() if pool is None else pool
-        return ccc.ssm_update(self.token, self.weight, conv, self.dt, self.g.A, pool, self.slots, n_groups=2, out=out, **self.par), conv, pool
+        return ccc.ssm_update(self.token, self.weight, conv, self.dt, self.g.A, pool, self.slots, n_groups=2, **self.par), conv, pool
 
     def all(self):
         return [*self.forward(), *self.backward(), *self.step()]
@@ -110,3 +110,39 @@ def test_scan_waits_run_out(name, no_patience):
         before = count
         assert all(torch.equal(a, b) for a, b in zip(want, run()))
         assert ccc.given_up_waits() == before
+
+
+def test_step_waits_run_out(no_patience):
+    """A warp that has no state stores none: every row of the pool has its old or its right value.  Many
+    heads a group, whose states come in pieces one behind another, so that some are looked for before they are there."""
+    ccc.set_wait_limit()
+    H, P, G, N, seqs = 48, 64, 4, 128, 200
+    gen = torch.Generator(device="cuda").manual_seed(83)
+    C = H * P + 2 * G * N
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device="cuda")
+    pool, conv = normal(seqs, H, P, N), normal(seqs, C, 3).bfloat16()
+    token, weight, dt, A = normal(seqs, C).bfloat16(), normal(C, 4).bfloat16(), normal(seqs, H), -normal(H).abs()
+    slots = torch.randperm(seqs, generator=gen, device="cuda").to(torch.int32)
+
+    def step():
+        a, b = conv.clone(), pool.clone()
+        return ccc.ssm_update(token, weight, a, dt, A, b, slots, n_groups=G, dt_softplus=True), a, b
+    y, conv_after, after = step()
+    before = ccc.given_up_waits()
+    for _ in range(3):
+        ccc.set_wait_limit(0)
+        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        begin.record()
+        got = step()[2]
+        end.record()
+        ccc.set_wait_limit()
+        count = ccc.given_up_waits()
+        assert count > before
+        # a drain that waits for what was never started takes a second
+        assert begin.elapsed_time(end) < 100.0
+        before = count
+        left, right = (got == pool).all(-1), (got == after).all(-1)
+        assert bool((left | right).all()) and not bool(right.all())
+        assert all(torch.equal(a, b) for a, b in zip((y, conv_after, after), step())) and ccc.given_up_waits() == before
