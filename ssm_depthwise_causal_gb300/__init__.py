@@ -142,18 +142,15 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _under_stream(call):
-    """A function that makes tensors and takes ``stream=`` runs under that stream: what it makes (workspace, offsets, flat
-    copies, results) is allocated, written and freed in its order, not in the current stream's."""
-    @functools.wraps(call)
-    def under(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_stream(stream))
-        with torch.cuda.stream(stream):
-            return call(*args, **kw)
-    return under
+def _under_stream(stream, call, args):
+    """``call`` with ``args`` but for their "stream", under that stream: what it makes (workspace, offsets, flat copies,
+    results) is allocated, written and freed in its order, not in the current stream's.  For functions that make tensors
+    and are given ``stream=``."""
+    args.pop("stream", None)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream))
+    with torch.cuda.stream(stream):
+        return call(**args)
 
 
 def _rows_view(t: torch.Tensor, name: str):
@@ -286,7 +283,8 @@ def ccc_check(rows, cu_seqlens, cache_indices=None, n_slots=0, num_accepted=None
     N = cu_seqlens.numel() - 1
     words = int(_lib.lib().ccc_check_status_words(int(n_slots))) if cache_indices is not None else 1
     if status is None:
-        status = _under_stream(torch.empty)(words, dtype=torch.int32, device=cu_seqlens.device, stream=stream)
+        make = functools.partial(torch.empty, words, dtype=torch.int32, device=cu_seqlens.device)
+        status = make() if stream is None else _under_stream(stream, make, {})
     if status.dtype != torch.int32 or not status.is_contiguous():
         raise ValueError("status must be a contiguous int32 tensor")
     _on_current_device(cu_seqlens, cache_indices, num_accepted, status)
@@ -332,14 +330,15 @@ def _packed(x, cu_seqlens):
     return x2, cu_seqlens, (lambda t: t.view(x.shape) if x.dim() == 3 else t)
 
 
-@_under_stream
 def causal_conv1d_fn(x, weight, conv_state=None, cu_seqlens=None, cache_indices=None,
                      has_initial_state=None, *, bias=None, activation="silu", out=None,
-                     workspace=None, saved_hist=None) -> torch.Tensor:
+                     workspace=None, saved_hist=None, stream=None) -> torch.Tensor:
     """Allocating forward: ``out`` and the workspace are created when omitted
     (rows past cu_seqlens[-1] of an ``out`` made here hold whatever the
     allocator left).  ``x`` is
     packed ``[rows, C]`` with ``cu_seqlens``, or ``[B, T, D]``."""
+    if stream is not None:
+        return _under_stream(stream, causal_conv1d_fn, locals())
     x2, cu, unpack = _packed(x, cu_seqlens)
     rows, C = x2.shape
     N = cu.numel() - 1
@@ -350,13 +349,14 @@ def causal_conv1d_fn(x, weight, conv_state=None, cu_seqlens=None, cache_indices=
     return unpack(o2) if out is None else out
 
 
-@_under_stream
 def causal_conv1d_bwd(x, weight, dy, cu_seqlens=None, *, bias=None, activation="silu",
                       saved_hist=None, cache_indices=None, has_initial_state=None,
-                      d_final_state=None, dx=None, want_d_init=False, workspace=None):
+                      d_final_state=None, dx=None, want_d_init=False, workspace=None, stream=None):
     """Allocating backward: returns ``(dx, dweight, dbias, d_init_state)``
     (dweight FP32 [C, W]; dbias None without a bias, d_init_state
     [N, W-1, C] only when requested)."""
+    if stream is not None:
+        return _under_stream(stream, causal_conv1d_bwd, locals())
     x2, cu, unpack = _packed(x, cu_seqlens)
     g2, _, _ = _packed(dy, cu_seqlens)
     rows, C = x2.shape
@@ -373,12 +373,14 @@ def causal_conv1d_bwd(x, weight, dy, cu_seqlens=None, *, bias=None, activation="
     return (unpack(d2) if dx is None else dx), dweight, dbias, d_init
 
 
-@_under_stream
 def causal_conv1d_update(x, weight, conv_state, cache_indices, *, cu_seqlens=None,
-                         num_accepted=None, bias=None, activation="silu", out=None) -> torch.Tensor:
+                         num_accepted=None, bias=None, activation="silu", out=None,
+                         stream=None) -> torch.Tensor:
     """Allocating decode step: ``x`` is ``[B, k, D]`` (k new tokens for each
     of B sequences; [B, D] means k = 1) or packed ``[rows, C]`` with
     ``cu_seqlens``; ``conv_state`` is updated in place (ccc_update)."""
+    if stream is not None:
+        return _under_stream(stream, causal_conv1d_update, locals())
     squeeze = x.dim() == 2 and cu_seqlens is None
     if squeeze:
         x = x.unsqueeze(1)   # [B, D]: one token per sequence
@@ -394,9 +396,8 @@ def causal_conv1d_update(x, weight, conv_state, cache_indices, *, cu_seqlens=Non
     return y
 
 
-@_under_stream
 def recompute_fwd(x, weight, saved_hist, cu_seqlens, cache_indices=None, *, bias=None,
-                  activation="silu", out=None, workspace=None) -> torch.Tensor:
+                  activation="silu", out=None, workspace=None, stream=None) -> torch.Tensor:
     """Re-run the forward from the history a previous ccc_fwd saved.
 
     ``saved_hist`` [N, W-1, C] is read as a pool of N slots (slot n =
@@ -405,6 +406,8 @@ def recompute_fwd(x, weight, saved_hist, cu_seqlens, cache_indices=None, *, bias
     since (the checkpoint recompute of ``cake_causal_conv1d_kcp``,
     recompute_handle).  ``saved_hist`` itself is not modified: the final state
     is written into a scratch copy."""
+    if stream is not None:
+        return _under_stream(stream, recompute_fwd, locals())
     N = cu_seqlens.numel() - 1
     pool = saved_hist.clone().transpose(1, 2)     # [N, C, W-1] view, channel axis contiguous
     slots = torch.arange(N, dtype=torch.int32, device=x.device)

@@ -53,7 +53,7 @@ def ccc_gated_norm_workspace_size(rows, width, group_size) -> int:
 # of include/ccc.h): packing them costs a fraction of converting each one.
 _PACK = {n: struct.Struct(f"{n}q").pack for n in (14, 21, 33, 38, 42)}
 
-_F32, _BF16 = torch.float32, torch.bfloat16
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 _CODE = {torch.float32: 0, torch.bfloat16: 1}
 
 
@@ -123,11 +123,15 @@ def _parameters(A, D, dt_bias, H) -> int:
     return _code(A, "A, D and dt_bias")
 
 
-def _metadata(t, name, need, types=(torch.int32,)) -> None:
-    """The library gets a bare pointer: a tensor of another type, layout or of fewer elements would be read as something else."""
-    if t is not None and (t.dtype not in types or t.numel() < need or not t.is_contiguous()):
-        what = " or ".join(str(v).removeprefix("torch.") for v in types)
-        raise ValueError(f"{name} must be contiguous {what} of {need} elements, got {t.dtype} {tuple(t.shape)}")
+# The library gets bare pointers: a tensor of another type or layout or of fewer elements would be read as something else.
+def _ints(t, name, need) -> None:
+    if t is not None and (t.dtype is not _I32 or t.numel() < need or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous int32 of {need} elements, got {t.dtype} {tuple(t.shape)}")
+
+
+def _flags(t, name, need) -> None:
+    if t is not None and (t.dtype not in (torch.bool, torch.uint8) or t.numel() < need or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous bool or uint8 of {need} elements, got {t.dtype} {tuple(t.shape)}")
 
 
 class _Batch:
@@ -154,7 +158,7 @@ class _Batch:
         if b_sizes[0] != rows or c_sizes != b_sizes:
             raise ValueError("x [rows, H, P], B and C [rows, G, N] do not match")
         self.seqs = cu_seqlens.numel() - 1
-        _metadata(cu_seqlens, "cu_seqlens", 1)
+        _ints(cu_seqlens, "cu_seqlens", 1)
         self.args = (x.data_ptr(), rows, H, P, xs, dt.data_ptr(), _code(dt, "dt"), _steps(dt, rows, H), 1 if dt_softplus else 0,
                      A.data_ptr(), _at(D), _at(dt_bias), _parameters(A, D, dt_bias, H), B.data_ptr(), bs, C.data_ptr(), cs, G, N)
 
@@ -193,10 +197,9 @@ def _bytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-@_under_stream
 def selective_scan_fn(x, dt, A, B, C, ssm_state=None, cu_seqlens=None, cache_indices=None, has_initial_state=None, *,
                       D=None, dt_bias=None, dt_softplus=False, initial_state=None, final_state=None, out=None,
-                      workspace=None) -> torch.Tensor:
+                      workspace=None, stream=None) -> torch.Tensor:
     """Selective scan forward (include/ccc.h, ccc_scan_fwd): y, shaped as x.
 
     ``x`` [rows, H, P], ``dt`` [rows, H], ``B`` and ``C`` [rows, G, N] are
@@ -204,6 +207,8 @@ def selective_scan_fn(x, dt, A, B, C, ssm_state=None, cu_seqlens=None, cache_ind
     buffer.  ``ssm_state`` is the FP32 slot pool [slots, H, P, N], updated in
     place (a pool with draft positions is passed as ``pool[:, 0]``); without
     one, ``initial_state`` / ``final_state`` are [N, H, P, N_state]."""
+    if stream is not None:
+        return _under_stream(stream, selective_scan_fn, locals())
     b = _Batch(x, dt, A, B, C, cu_seqlens, D, dt_bias, dt_softplus)
     H, P, N = b.H, b.P, b.N
     slots, st_slot = 0, 0
@@ -212,8 +217,8 @@ def selective_scan_fn(x, dt, A, B, C, ssm_state=None, cu_seqlens=None, cache_ind
         if ssm_state.dtype != _F32 or ssm_state.shape[1:] != (H, P, N) or not (slots == 0 or ssm_state[0].is_contiguous()):
             raise ValueError("ssm_state must be FP32 [slots, H, P, N] with contiguous slots")
         st_slot = ssm_state.stride(0) if slots > 1 else H * P * N
-    _metadata(cache_indices, "cache_indices", b.seqs)
-    _metadata(has_initial_state, "has_initial_state", b.seqs, (torch.bool, torch.uint8))
+    _ints(cache_indices, "cache_indices", b.seqs)
+    _flags(has_initial_state, "has_initial_state", b.seqs)
     o = b.place(out, (b.rows, H, P), "out")
     os = H * P if out is None else _rows3(o, "out", (b.rows, H, P), "out must match x")
     b.states(initial_state, "initial_state")
@@ -229,10 +234,9 @@ def selective_scan_fn(x, dt, A, B, C, ssm_state=None, cu_seqlens=None, cache_ind
     return b.unflat(o) if out is None else out
 
 
-@_under_stream
 def selective_scan_bwd(x, dt, A, B, C, dy, cu_seqlens=None, *, D=None, dt_bias=None, dt_softplus=False, initial_state=None,
                        cache_indices=None, d_final_state=None, want_d_initial=False, carry_empty=False, dx=None, dB=None,
-                       dC=None, workspace=None) -> ScanGrads:
+                       dC=None, workspace=None, stream=None) -> ScanGrads:
     """Selective scan backward (include/ccc.h, ccc_scan_bwd).  ``dx``, ``dB``
     and ``dC`` may be given, also as column slices of one buffer (the dy of
     ccc_bwd); rows past cu_seqlens[-1] of what is made here are not written.
@@ -240,8 +244,10 @@ def selective_scan_bwd(x, dt, A, B, C, dy, cu_seqlens=None, *, D=None, dt_bias=N
     adds that of an empty sequence, whose final state is its initial one (its
     d_final_state as it is): pass it where fragments are chained, as the
     autograd wrapper does."""
+    if stream is not None:
+        return _under_stream(stream, selective_scan_bwd, locals())
     b = _Batch(x, dt, A, B, C, cu_seqlens, D, dt_bias, dt_softplus)
-    _metadata(cache_indices, "cache_indices", b.seqs)
+    _ints(cache_indices, "cache_indices", b.seqs)
     wide, narrow, new = (b.rows, b.H, b.P), (b.rows, b.G, b.N), b.x.new_empty
     dy2, dx2, dB2, dC2 = b.flat(dy), b.place(dx, wide, "dx"), b.place(dB, narrow, "dB"), b.place(dC, narrow, "dC")
     match = "dy and dx must match x, dB and dC must match B"
@@ -304,15 +310,16 @@ def selective_scan(x, dt, A, B, C, cu_seqlens=None, *, D=None, dt_bias=None, dt_
     return SelectiveScanFn.apply(x, dt, A, B, C, D, dt_bias, initial_state, cu_seqlens, cache_indices, dt_softplus)
 
 
-@_under_stream
 def ssm_update(xBC, weight, conv_state, dt, A, ssm_state, cache_indices, *, n_groups, cu_seqlens=None, num_accepted=None,
-               bias=None, activation="silu", D=None, dt_bias=None, dt_softplus=False, out=None) -> torch.Tensor:
+               bias=None, activation="silu", D=None, dt_bias=None, dt_softplus=False, out=None, stream=None) -> torch.Tensor:
     """One decode step of the mixer (include/ccc.h, ccc_ssm_update): y
     [rows, H, P] (or [B, k, H, P]) of the new tokens ``xBC`` [rows, C] with
     ``cu_seqlens`` ([B, C]: one token a request; [B, k, C]: k of them), with
     both pools updated in place.  ``ssm_state`` is [slots, H, P, N] for one
     token a request, or [slots, positions, H, P, N] to keep the states after a
     request's first ``positions`` tokens (of which num_accepted then names one)."""
+    if stream is not None:
+        return _under_stream(stream, ssm_update, locals())
     lead = None
     if xBC.dim() == 3:
         lead = xBC.shape[:2]
@@ -324,9 +331,10 @@ def ssm_update(xBC, weight, conv_state, dt, A, ssm_state, cache_indices, *, n_gr
         cu_seqlens = torch.arange(xBC.shape[0] + 1, dtype=torch.int32, device=xBC.device)
     xs, (rows, channels) = _rows2s(xBC, "xBC")
     seqs = cu_seqlens.numel() - 1
-    _metadata(cu_seqlens, "cu_seqlens", 1)
-    _metadata(cache_indices, "cache_indices", seqs)
-    _metadata(num_accepted, "num_accepted", seqs)
+    _ints(cu_seqlens, "cu_seqlens", 1)
+    _ints(cache_indices, "cache_indices", seqs)
+    if num_accepted is not None:
+        _ints(num_accepted, "num_accepted", seqs)
     if ssm_state.dtype != _F32 or ssm_state.dim() not in (4, 5):
         raise ValueError("ssm_state must be FP32 [slots, H, P, N] or [slots, positions, H, P, N]")
     G = int(n_groups)
@@ -391,10 +399,11 @@ def _norm_args(y, z, weight, group_size, eps, norm_before_gate):
             1 if norm_before_gate else 0), sizes
 
 
-@_under_stream
-def gated_rms_norm_fn(y, z, weight, *, eps=1e-5, group_size=None, norm_before_gate=False, out=None) -> torch.Tensor:
+def gated_rms_norm_fn(y, z, weight, *, eps=1e-5, group_size=None, norm_before_gate=False, out=None, stream=None) -> torch.Tensor:
     """Gated RMS norm (include/ccc.h, ccc_gated_norm_fwd) of y by the gate z,
     both BF16 [..., width]; ``group_size`` defaults to the whole width."""
+    if stream is not None:
+        return _under_stream(stream, gated_rms_norm_fn, locals())
     y2, z2 = _flat2(y), _flat2(z)
     args, sizes = _norm_args(y2, z2, weight, group_size, eps, norm_before_gate)
     if out is None:
@@ -409,10 +418,11 @@ def gated_rms_norm_fn(y, z, weight, *, eps=1e-5, group_size=None, norm_before_ga
     return out if out is not None else o if y2 is y else o.view(y.shape)
 
 
-@_under_stream
 def gated_rms_norm_bwd(y, z, weight, dout, *, eps=1e-5, group_size=None, norm_before_gate=False, dy=None, dz=None,
-                       workspace=None):
+                       workspace=None, stream=None):
     """(dy, dz, dweight) of gated_rms_norm_fn; dweight is FP32 [width]."""
+    if stream is not None:
+        return _under_stream(stream, gated_rms_norm_bwd, locals())
     y2, z2, g2 = _flat2(y), _flat2(z), _flat2(dout)
     args, sizes = _norm_args(y2, z2, weight, group_size, eps, norm_before_gate)
     gs = _rows2(g2, "dout", sizes, "dout must match y")
@@ -459,7 +469,8 @@ def ccc_wait_status(status=None, stream=None) -> torch.Tensor:
     first element receives the count once the stream gets there (no synchronization here).  Anything but 0: results of the
     scans and decode steps since it was 0 are undefined."""
     if status is None:
-        status = _under_stream(torch.empty)(1, dtype=torch.int32, device="cuda", stream=stream)
+        make = functools.partial(torch.empty, 1, dtype=torch.int32, device="cuda")
+        status = make() if stream is None else _under_stream(stream, make, {})
     if status.dtype is not torch.int32 or status.numel() < 1 or not status.is_contiguous():
         raise ValueError("status must be a contiguous int32 tensor")
     _on_current_device(status)
