@@ -385,9 +385,13 @@ int ccc_check(int64_t rows, const int32_t *cu_seqlens, int32_t N,
  * x, B and C may be column slices of one row buffer (the output of ccc_fwd),
  * and so may dx, dB and dC.  The state, the sums and the running products are
  * FP32.  Sizes of N_state <= 128 and P <= 64 or P % 64 == 0 go to the tensor
- * cores with BF16 operands: what the forward adds to a state is given to them as
- * two BF16 parts (16 bits a term), in the backward states and state gradients as
- * three (all 24).  An infinity or NaN in a sequence's inputs makes that
+ * cores with BF16 operands.  States keep 16 bits (two BF16 parts) of each term in
+ * the forward and all 24 (three) in the backward, whose dt, A, D and bias gradients
+ * are made of 32-bit products.  What leaves in 16 bits is less exact on the way:
+ * in y, dx, dB and dC the decayed products of C and B (of dy and x) are rounded to
+ * BF16 once before they are multiplied by x (dy, B, C), y's C h takes h rounded
+ * to BF16, and dx's state term the gradient of the state in 16 bits.  Other sizes
+ * are computed in FP32 throughout.  An infinity or NaN in a sequence's inputs makes that
  * sequence's outputs undefined from the start of its 128-token chunk on; in the
  * backward all of that sequence's gradients, and the sums over all tokens.
  * Other sequences are not touched by it, nor by what lies in rows past

@@ -15,6 +15,11 @@
 // and the reverse one has M = T1 L for dx besides.  Each row's share of the
 // decays' gradient is the row sum of T1 T2 L, which stays in FP32, and Q_i.(U E)_i
 // with all parts of E; that way both orientations of the sums are a thread's own.
+// Rounded to BF16, once each: W and M, as operands of products whose results leave
+// in 16 bits (dC, dB, dx), where they cost a unit roundoff of each term.  U E has all
+// 24 bits of the state; dx's G B has two parts of G, 16 bits: the second one makes
+// dx's state term as good as its own rounding (one part: off by a unit more) and
+// takes no measurable time, a third one 4 of 601 us.
 // dt, A, D and dt_bias follow from them (finish_kernel):
 // d(dt A)_t is the sum over all pairs (s, u) with s < t <= u of what s gives to
 // u, for s before the chunk and u behind it too.  For pairs of one block of 32
@@ -262,12 +267,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     tc_fence_after();
                     if (tc_elect()) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {  // the two parts of dx in turn
+                        for (int i = 0; i < 8; ++i) {  // dx: M dy, and B G^T with two parts of G, in turn
                             tc_mma_ts(tmem + kColE, tmem + kColW + i * 16 + 8, tc_desc(sv + i * 2048, kTile, 1024),
                                       tc_idesc(64, false, true), i > 0);
-                            if (i < 4 * NB)
+#pragma unroll
+                            for (int part = 0; part < 2 && i < 4 * NB; ++part)
                                 tc_mma_ss(tmem + kColE + 64, tc_desc(sq + (i / 4) * kTile + (i % 4) * 32, 16, 1024),
-                                          tc_desc(se + (i / 4) * (kTile / 2) + (i % 4) * 32, 16, 1024), tc_idesc(64, false, false), i > 0);
+                                          tc_desc(se + part * kTile + (i / 4) * (kTile / 2) + (i % 4) * 32, 16, 1024), tc_idesc(64, false, false),
+                                          i > 0 || part > 0);
                         }
                         tc_commit(bar(kDxFull));
                     }
