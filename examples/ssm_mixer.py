@@ -32,7 +32,9 @@ class Mixer(nn.Module):
 
         def weight(*shape):
             return nn.Parameter((torch.randn(shape, generator=g) * shape[-1] ** -0.5).bfloat16())
-        self.w_in = weight(self.inner + self.channels + H, width)  # z | x B C | dt
+        # z | x B C | dt, and unused columns up to a multiple of eight: z and x are read with the projection's row stride
+        self.parts = [self.inner, self.channels, H, -H % 8]
+        self.w_in = weight(sum(self.parts), width)
         self.w_out = weight(width, self.inner)
         self.conv_w = nn.Parameter(torch.rand(self.channels, 4, generator=g) - 0.5)
         self.conv_b = nn.Parameter(torch.zeros(self.channels))
@@ -42,7 +44,7 @@ class Mixer(nn.Module):
         self.norm_w = nn.Parameter(torch.ones(self.inner))
 
     def project(self, hidden):
-        return (hidden @ self.w_in.t()).split([self.inner, self.channels, self.sizes[0]], dim=1)
+        return (hidden @ self.w_in.t()).split(self.parts, dim=1)[:3]
 
     def heads(self, xbc):
         H, P, G, N = self.sizes
