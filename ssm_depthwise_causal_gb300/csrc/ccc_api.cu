@@ -71,8 +71,6 @@ bool state_layout_ok(int n_slots, int C, int L, int64_t s_slot, int64_t s_c, int
 
 void set_last_launches(int n) { g_last_launches = n; }
 
-int device_sms() { return device_facts().sms; }
-
 }  // namespace ccc
 
 extern "C" {

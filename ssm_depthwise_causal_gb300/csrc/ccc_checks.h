@@ -49,9 +49,6 @@ bool state_layout_ok(int n_slots, int C, int L, int64_t s_slot, int64_t s_c, int
 // What ccc_last_launch_count reports for this host thread.
 void set_last_launches(int n);
 
-// Multiprocessors of the current device, queried once a device (152 where that fails).
-int device_sms();
-
 // f with its arguments from an array of 64-bit integers (the _v entry points).
 template <class T>
 T unpacked(int64_t v) {
