@@ -86,7 +86,6 @@ __device__ __forceinline__ float dt_value(const ScanArgs &a, uint32_t bits) { re
 struct Chunk {
     int n, len;
     int64_t row;
-    bool first, last;
 };
 
 __device__ __forceinline__ Chunk scan_chunk(const ScanArgs &a, int64_t slot, int q) {
@@ -97,7 +96,7 @@ __device__ __forceinline__ Chunk scan_chunk(const ScanArgs &a, int64_t slot, int
     }
     const Seq s = scan_seq(a, lo);
     const int64_t row = s.begin + (slot - s.begin / q - lo) * q;
-    Chunk c{lo, 0, row, row == s.begin, row + q >= s.end};
+    Chunk c{lo, 0, row};
     if (row >= s.begin && row < s.end) c.len = static_cast<int>(min(static_cast<int64_t>(q), s.end - row));
     return c;
 }
