@@ -417,7 +417,13 @@ int ccc_check(int64_t rows, const int32_t *cu_seqlens, int32_t N,
  *  out          [dev] BF16 [rows][out_row_stride], must not overlap any
  *               operand; rows after cu_seqlens[N] are not written.
  *  workspace    [dev] >= ccc_scan_workspace_size(..., 0) bytes, 256-byte
- *               aligned; need not be initialised.  Should a kernel ever give up
+ *               aligned; need not be initialised.  For the tensor-core sizes at
+ *               most 20 MB forward; backward (..., 1) some 220 KB for each 128
+ *               tokens of a sequence (or part of them) and two heads of 64, with
+ *               N_state > 64 (120 KB with less): states and state gradients.
+ *               16384 tokens of 32 heads: 0.48 GB; 65536 of 96: 5.4 GB; a million
+ *               of 32: 28 GB.  A document in fragments (initial_state,
+ *               d_final_state) needs a fragment's at a time.  Should a kernel ever give up
  *               one of its bounded internal waits (ccc_wait_status), the
  *               workspace's first 32-bit word is set to 1; the calls do not clear
  *               that word.

@@ -204,7 +204,8 @@ def selective_scan_fn(x, dt, A, B, C, ssm_state=None, cu_seqlens=None, cache_ind
 
     ``x`` [rows, H, P], ``dt`` [rows, H], ``B`` and ``C`` [rows, G, N] are
     packed by ``cu_seqlens`` (or [B, T, ...]), and may be column slices of one
-    buffer.  ``ssm_state`` is the FP32 slot pool [slots, H, P, N], updated in
+    buffer; rows past cu_seqlens[-1] of a y made here are not written.
+    ``ssm_state`` is the FP32 slot pool [slots, H, P, N], updated in
     place (a pool with draft positions is passed as ``pool[:, 0]``); without
     one, ``initial_state`` / ``final_state`` are [N, H, P, N_state]."""
     if stream is not None:
