@@ -58,9 +58,10 @@ __device__ __forceinline__ void load_rows(uint16_t *dst, int pitch, const uint16
     }
 }
 
-// dt, its slope and the running sum of dt A log2(e) of a chunk's tokens; past the end dt = 0.
+// dt, its slope, the running sum of dt A log2(e) of a chunk's tokens and the sum behind each (the decay from a token to the
+// chunk's end: a sum of its own, as the difference of two long running sums would lose its bits); past the end dt = 0.
 struct Steps {
-    float dt[Q], slope[Q], a[Q];
+    float dt[Q], slope[Q], a[Q], after[Q];
 };
 
 __device__ __forceinline__ void load_steps(const ScanArgs &a, int h, int64_t row, int len, Steps &s) {
@@ -68,18 +69,22 @@ __device__ __forceinline__ void load_steps(const ScanArgs &a, int h, int64_t row
         const int t = threadIdx.x;
         float dt = 0.0f, slope = 0.0f;
         if (t < len) dt = scan_dt(a, row + t, h, a.dt_bias ? par(a.dt_bias, a.p_bf16, h) : 0.0f, &slope);
-        float v = dt * par(a.A, a.p_bf16, h) * kLog2e;
+        float v = dt * par(a.A, a.p_bf16, h) * kLog2e, w = v;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const float o = __shfl_up_sync(kFull, v, d);
+            const float o = __shfl_up_sync(kFull, v, d), u = __shfl_down_sync(kFull, w, d);
             if ((t & 31) >= d) v += o;
+            if ((t & 31) + d < 32) w += u;
         }
         s.dt[t] = dt;
         s.slope[t] = slope;
         s.a[t] = v;
+        s.after[t ? t - 1 : Q - 1] = t ? w : 0.0f;
     }
     __syncthreads();
+    static_assert(Q == 64, "two warps");
     if (threadIdx.x >= 32 && threadIdx.x < Q) s.a[threadIdx.x] += s.a[31];
+    if (threadIdx.x < 31) s.after[threadIdx.x] += s.after[31];
     __syncthreads();
 }
 
@@ -128,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const ScanArgs a, bool
         load_rows(vs, pv, (reverse ? a.dy : a.x) + h * P, reverse ? a.dy_rs : a.x_rs, row, len, P);
         load_steps(a, h, row, len, st);
         const float end = st.a[Q - 1], keep = ex2_approx(end);
-        if (threadIdx.x < Q) st.slope[threadIdx.x] = reverse ? ex2_approx(st.a[threadIdx.x]) : ex2_approx(end - st.a[threadIdx.x]) * st.dt[threadIdx.x];
+        if (threadIdx.x < Q) st.slope[threadIdx.x] = reverse ? ex2_approx(st.a[threadIdx.x]) : ex2_approx(st.after[threadIdx.x]) * st.dt[threadIdx.x];
         __syncthreads();
         const float *from = ws + (slot0 + c) * hpn + head;
         float *to = i + 1 == chunks ? (leave ? leave + head : nullptr) : ws + (slot0 + c + (reverse ? -1 : 1)) * hpn + head;
@@ -248,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) chunks_bwd_kernel(const ScanArgs a) 
             }
             if (tid % 32 == 0) {
                 s_in[t] = in * ex2_approx(st.a[t]);
-                s_out[t] = out * ex2_approx(end - st.a[t]);  // without dt_s
+                s_out[t] = out * ex2_approx(st.after[t]);  // without dt_s
             }
         }
         // <G, S>, in a fixed order
@@ -287,11 +292,11 @@ __global__ void __launch_bounds__(kThreads) chunks_bwd_kernel(const ScanArgs a) 
         __syncthreads();
         if (tid < 3) a.part[(slot * a.H + h) * 3 + tid] = s_tmp[tid] + s_tmp[32 + tid];
         uint16_t *dx = a.dx + c.row * a.dx_rs + h * P;
-        product(Q, P, Q + N, [&](int s, int k) { return k < Q ? m[k * pm + s] : ex2_approx(end - st.a[s]) * bf_to_f(bs[s * pk + k - Q]); },
+        product(Q, P, Q + N, [&](int s, int k) { return k < Q ? m[k * pm + s] : ex2_approx(st.after[s]) * bf_to_f(bs[s * pk + k - Q]); },
                 [&](int p, int k) { return k < Q ? bf_to_f(ys[k * pv + p]) : G[p * N + k - Q]; },
                 [&](int s, int p, float v) { if (s < c.len) dx[s * a.dx_rs + p] = f_to_bf(fmaf(D, bf_to_f(ys[s * pv + p]), v * st.dt[s])); });
         // dB_s and dC_t: sums over the group's heads in FP32, the same thread's elements each time
-        product(Q, N, Q + P, [&](int s, int k) { return k < Q ? w[k * pm + s] : ex2_approx(end - st.a[s]) * bf_to_f(xs[s * pv + k - Q]); },
+        product(Q, N, Q + P, [&](int s, int k) { return k < Q ? w[k * pm + s] : ex2_approx(st.after[s]) * bf_to_f(xs[s * pv + k - Q]); },
                 [&](int j, int k) { return k < Q ? bf_to_f(cs[k * pk + j]) : G[(k - Q) * N + j]; },
                 [&](int s, int j, float v) {
                     if (s >= c.len) return;

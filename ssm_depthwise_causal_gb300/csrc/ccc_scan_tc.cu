@@ -42,8 +42,9 @@
 // own running sums p; from block j to a later block q
 //     2^(a_t - a_s) = [2^(P_j - p_s)] [2^(p_t + P_j+1 + .. + P_q-1)],
 // P the blocks' totals: one exponential per s, three per t, in place of one per
-// pair, neither factor above one for a decaying state, and no exponent is a
-// difference of long sums.
+// pair, neither factor above one for a decaying state.  P_j - p_s, like the decay
+// to the chunk's end, is a sum over the tokens behind s, not that difference; within
+// a block of 32, p_t - p_s is one of sums of 32 (M leaves in 8 bits).
 #include <algorithm>
 
 #include "ccc_checks.h"
@@ -263,19 +264,20 @@ __global__ void __launch_bounds__(kThreads, 1) walk_kernel(const __grid_constant
                 bias = mine.ok && a.s.dt_bias ? par(a.s.dt_bias, a.s.p_bf16, mine.h) : 0.0f;
             }
             more = fetch(k + 1, next);
-            float dt[4], p[4], P[4], after = 0.0f;
+            float dt[4], v[4], p[4], P[4], to_end[4], after = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 dt[i] = mine.ok && 32 * i + lane < len ? step_of(dt_value(a.s, raw[i]) + bias, a.s.softplus) : 0.0f;
-                p[i] = dt[i] * A2;
+                v[i] = p[i] = dt[i] * A2;
             }
             block_sums(p, P);
+            block_after(v, p, P, to_end);
             bar_wait(bar(kArrays0 + (k & 1)), ((k >> 1) & 1) ^ 1, failed);
             Arrays &r = arrays[k & 1];
 #pragma unroll
             for (int i = 3; i >= 0; --i) {
                 const int t = 32 * i + lane;
-                const float c = dt[i] * ex2_approx(P[i] - p[i]);
+                const float c = dt[i] * ex2_approx(to_end[i]);
                 r.p[hd][t] = p[i];
                 r.dt[hd][t] = dt[i];
                 r.c[hd][t] = c;

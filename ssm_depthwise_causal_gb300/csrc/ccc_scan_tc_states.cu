@@ -195,20 +195,21 @@ __global__ void __launch_bounds__(kThreads, 1) states_kernel(const __grid_consta
                     bias = mine.ok && a.s.dt_bias ? par(a.s.dt_bias, a.s.p_bf16, mine.h) : 0.0f;
                 }
                 more = fetch(k + 1, next);
-                float dt[4], p[4], P[4];
+                float dt[4], v[4], p[4], P[4], to_end[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     dt[i] = mine.ok && 32 * i + lane < len ? step_of(dt_value(a.s, raw[i]) + bias, a.s.softplus) : 0.0f;
-                    p[i] = dt[i] * A2;
+                    v[i] = p[i] = dt[i] * A2;
                 }
                 block_sums(p, P);
+                if (!REV) block_after(v, p, P, to_end);
                 bar_wait(bar(kArrays0 + (k & 1)), ((k >> 1) & 1) ^ 1, failed);
                 Arrays &r = arrays[k & 1];
                 // the blocks before (reverse) or after a block, with the distance inside it
-                r.w[hd][lane] = REV ? ex2_approx(p[0]) : dt[0] * ex2_approx((P[0] - p[0]) + (P[1] + (P[2] + P[3])));
-                r.w[hd][32 + lane] = REV ? ex2_approx(P[0] + p[1]) : dt[1] * ex2_approx((P[1] - p[1]) + (P[2] + P[3]));
-                r.w[hd][64 + lane] = REV ? ex2_approx((P[0] + P[1]) + p[2]) : dt[2] * ex2_approx((P[2] - p[2]) + P[3]);
-                r.w[hd][96 + lane] = REV ? ex2_approx((P[0] + P[1] + P[2]) + p[3]) : dt[3] * ex2_approx(P[3] - p[3]);
+                r.w[hd][lane] = REV ? ex2_approx(p[0]) : dt[0] * ex2_approx(to_end[0] + (P[1] + (P[2] + P[3])));
+                r.w[hd][32 + lane] = REV ? ex2_approx(P[0] + p[1]) : dt[1] * ex2_approx(to_end[1] + (P[2] + P[3]));
+                r.w[hd][64 + lane] = REV ? ex2_approx((P[0] + P[1]) + p[2]) : dt[2] * ex2_approx(to_end[2] + P[3]);
+                r.w[hd][96 + lane] = REV ? ex2_approx((P[0] + P[1] + P[2]) + p[3]) : dt[3] * ex2_approx(to_end[3]);
                 if (lane < 4) r.total[hd][lane] = lane == 0 ? P[0] : lane == 1 ? P[1] : lane == 2 ? P[2] : P[3];
                 warp_arrive(bar(kSteps0 + (k & 1)));
 #pragma unroll
